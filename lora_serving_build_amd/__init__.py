@@ -10,6 +10,10 @@ points carry the C-ABI names of ``include/lora.h``:
     and the single-adapter forms lora_shrink_single, lora_expand_single,
     lora_expand_slice_single, lora_shrink_single_workspace_bytes
 
+and, in ``decode.py``, those of ``include/lora_decode.h``: the 4-bit base
+products (lora_q4_*), tree attention over a paged cache (lora_tree_attention)
+and the cache's page operations (lora_pages_*).
+
 If the shared library has not been built (``python -m
 lora_serving_build_amd.build``), every entry point raises: there is no
 fallback.
@@ -105,6 +109,7 @@ def lib() -> ctypes.CDLL:
                       "lora_expand_slice", "lora_shrink_single", "lora_expand_single",
                       "lora_expand_slice_single", "lora_shrink_expand"):
                 getattr(L, f).restype = ctypes.c_int
+            _declare_decode(L)
             _lib = L
     return _lib
 
@@ -448,3 +453,10 @@ def lora_expand_slice_single(v: torch.Tensor, Bs, col_offs, y: torch.Tensor, add
                                           offs, ns, r, T, ctypes.c_void_p(y.data_ptr()), ldy,
                                           int(bool(add_inputs)), _dtype_code(y.dtype), _stream(y.device)))
     return y
+
+
+# ---------------------------------------------------------------- decode step
+from .decode import *  # noqa: E402,F401,F403
+from .decode import __all__ as _decode_all, _declare as _declare_decode  # noqa: E402
+
+__all__ += _decode_all

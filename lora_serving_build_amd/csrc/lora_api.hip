@@ -14,8 +14,10 @@
 #include "lora_kernels.h"
 
 namespace {
-
 thread_local char g_error[512] = "";
+}
+
+namespace lora {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -34,6 +36,14 @@ int hip_status(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(LORA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
   return ok();
 }
+
+}  // namespace lora
+
+namespace {
+
+using lora::fail;
+using lora::hip_status;
+using lora::ok;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -8,6 +8,12 @@
 
 namespace lora {
 
+// Error reporting of the C-ABI layer (lora_api.hip): the thread's message and
+// the status the entry point returns.
+int fail(int code, const char* fmt, ...);
+int ok();
+int hip_status(hipError_t e, const char* what);
+
 constexpr int kMaxSlices = 8;
 constexpr int kMaxRank = 128;
 constexpr int kMaxLoras = 2048;

@@ -1,0 +1,552 @@
+// Page operations of a paged key / value cache (lora_pages_*): allocation,
+// reference counts, copies.
+//
+// Allocation is a scan of the reference counts for zeros by one workgroup:
+// there is no free list whose order could depend on timing, and releasing a
+// page is one atomic decrement.  Everything that moves cache rows runs as 16
+// bytes per lane over many workgroups.
+#include "decode_kernels.h"
+#include "lora_device.h"
+
+namespace lora {
+namespace {
+
+constexpr int kScanThreads = 1024;
+constexpr int kScanItems = 16;  // counts per thread and round: 64 KiB of counts a round
+constexpr int kOk = 0, kNoSpace = 1, kBad = 2;
+
+__device__ __forceinline__ bool in_range(int32_t v, int32_t n) { return (uint32_t)v < (uint32_t)n; }
+
+// Whether entry i names the same id as an earlier entry.  Every thread of the
+// block must call it.
+__device__ __forceinline__ bool repeated(const int32_t* __restrict__ ids, int i) {
+  bool same = false;
+  const int32_t id = ids[i];
+  for (int j = threadIdx.x; j < i; j += blockDim.x) same |= ids[j] == id;
+  return __syncthreads_or(same);
+}
+
+// Calls give(rank, page) for the first `total` free pages in ascending order,
+// rank 0 first.  Returns how many there were (at most total).  One block of
+// kScanThreads; scratch: kScanThreads / 64 + 1 ints.
+template <typename Give>
+__device__ __forceinline__ int scan_free(const int32_t* __restrict__ refs, int32_t num_pages, int total,
+                                         int* scratch, Give give) {
+  int found = 0;
+  for (int64_t base = 0; base < num_pages && found < total; base += kScanThreads * kScanItems) {
+    const int64_t p0 = base + (int64_t)threadIdx.x * kScanItems;
+    uint32_t zero = 0;
+#pragma unroll
+    for (int e = 0; e < kScanItems; ++e)
+      if (p0 + e < num_pages && refs[p0 + e] == 0) zero |= 1u << e;
+    int round;
+    int rank = found + block_exclusive_sum<kScanThreads>(__popc(zero), scratch, &round);
+    while (zero) {
+      const int e = __ffs(zero) - 1;
+      zero &= zero - 1;
+      if (rank < total) give(rank, (int32_t)(p0 + e));
+      ++rank;
+    }
+    found += round;
+  }
+  return found < total ? found : total;
+}
+
+// Number of leading entries >= 0 of a table row, by a whole wave: 64 probes a
+// step.
+__device__ __forceinline__ int row_pages(const int32_t* __restrict__ row, int max_pages) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int lo = 0, hi = max_pages;  // entries below lo are >= 0, the first < 0 is at or before hi
+  while (lo < hi) {
+    const int step = (hi - lo + kWave - 1) / kWave;
+    const int at = lo + lane * step;
+    const bool held = at < hi && row[at] >= 0;
+    const uint64_t m = __ballot(held);
+    const int leading = m == ~0ull ? kWave : __ffsll((unsigned long long)~m) - 1;
+    if (leading == 0) return lo;
+    const int last = lo + (leading - 1) * step;  // the last probe that was held
+    hi = last + step < hi ? last + step : hi;
+    lo = last + 1;
+  }
+  return lo;
+}
+
+// Pages of `tokens` tokens (tokens >= 0).
+__device__ __forceinline__ int64_t pages_of(int64_t tokens, int page_size) {
+  return (tokens + page_size - 1) / page_size;
+}
+
+// ---------------------------------------------------------------- resize
+__global__ void __launch_bounds__(kScanThreads) resize_kernel(PageView c, const int32_t* __restrict__ seqs,
+                                                              const int32_t* __restrict__ lens,
+                                                              const int32_t* __restrict__ extra, int n,
+                                                              int32_t* __restrict__ status) {
+  __shared__ int scratch[kScanThreads / kWave + 1];
+  __shared__ int32_t ids[kMaxPageEntries];
+  __shared__ int end[kMaxPageEntries];    // inclusive prefix of the pages needed
+  __shared__ int held[kMaxPageEntries];   // pages held before; -1: bad entry
+  __shared__ int want[kMaxPageEntries];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  for (int i = tid; i < n; i += kScanThreads) ids[i] = seqs[i];
+  __syncthreads();
+  for (int i = wave; i < n; i += kScanThreads / kWave) {
+    const int32_t s = ids[i];
+    bool same = false;
+    for (int j = lane; j < i; j += kWave) same |= ids[j] == s;
+    bool good = in_range(s, c.max_seqs) && !__any(same);
+    int have = 0;
+    int64_t need = 0;
+    if (good) {
+      const int32_t len = lens ? lens[i] : c.seq_len[s];
+      const int32_t more = extra ? extra[i] : 0;
+      need = pages_of((int64_t)len + more, c.page_size);
+      good = len >= 0 && more >= 0 && need <= c.max_pages;
+      if (good) have = row_pages(c.table + (int64_t)s * c.ld_table, c.max_pages);
+    }
+    if (lane == 0) {
+      held[i] = good ? have : -1;
+      want[i] = good ? (int)need : 0;
+    }
+  }
+  __syncthreads();
+  // Prefix sums of what each entry needs (a sum never passes 2^31: at most
+  // kMaxPageEntries rows of max_pages entries, which the host has checked).
+  int before = 0;
+  for (int base = 0; base < n; base += kScanThreads) {
+    const int i = base + tid;
+    const int need = i < n && held[i] >= 0 && want[i] > held[i] ? want[i] - held[i] : 0;
+    int sum;
+    const int excl = block_exclusive_sum<kScanThreads>(need, scratch, &sum);
+    if (i < n) end[i] = before + excl + need;
+    before += sum;
+  }
+  __syncthreads();
+  const int found = scan_free(c.refs, c.num_pages, before, scratch, [&](int rank, int32_t page) {
+    // The entry whose range of ranks holds this one.  Entries that turn out
+    // not to be served as a whole give their pages back below.
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (end[mid] > rank) hi = mid; else lo = mid + 1;
+    }
+    const int first = end[lo] - (want[lo] - held[lo]);
+    c.table[(int64_t)ids[lo] * c.ld_table + held[lo] + (rank - first)] = page;
+    c.refs[page] = 1;
+  });
+  __syncthreads();
+  for (int i = wave; i < n; i += kScanThreads / kWave) {
+    if (held[i] < 0) {
+      if (status && lane == 0) status[i] = kBad;
+      continue;
+    }
+    const int32_t s = ids[i];
+    int32_t* row = c.table + (int64_t)s * c.ld_table;
+    const bool grows = want[i] > held[i];
+    const bool fits = !grows || end[i] <= found;
+    // Release: the tail of a shrinking row, or the pages that an unserved
+    // entry received.
+    int from = want[i], to = held[i];
+    if (grows) {
+      const int first = end[i] - (want[i] - held[i]);
+      from = held[i];
+      to = fits || found <= first ? held[i] : held[i] + (found - first);
+    }
+    for (int w = from + lane; w < to; w += kWave) {
+      const int32_t p = row[w];
+      if (in_range(p, c.num_pages)) atomicSub(&c.refs[p], 1);
+      row[w] = -1;
+    }
+    if (lane == 0) {
+      if (lens && fits) c.seq_len[s] = lens[i];
+      if (status) status[i] = fits ? kOk : kNoSpace;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- copies
+// Whole pages: 256 lanes move 16 bytes each, kCopyUnroll loads in flight.
+constexpr int kCopyUnroll = 8;
+constexpr int kCopyBytes = 256 * 16 * kCopyUnroll;
+
+__device__ __forceinline__ void copy_span(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, int64_t bytes) {
+  u32x4 v[kCopyUnroll];
+  const int64_t at = (int64_t)threadIdx.x * 16;
+#pragma unroll
+  for (int u = 0; u < kCopyUnroll; ++u)
+    if (at + u * 4096 < bytes) v[u] = *reinterpret_cast<const u32x4*>(src + at + u * 4096);
+#pragma unroll
+  for (int u = 0; u < kCopyUnroll; ++u)
+    if (at + u * 4096 < bytes) *reinterpret_cast<u32x4*>(dst + at + u * 4096) = v[u];
+}
+
+__global__ void __launch_bounds__(256) copy_kernel(PageView c, const int32_t* __restrict__ src,
+                                                   const int32_t* __restrict__ dst, int64_t page_bytes, int spans) {
+  const int span = blockIdx.x % spans;
+  const int64_t pool = blockIdx.x / spans;
+  const int i = blockIdx.y;
+  const int32_t a = src[i], b = dst[i];
+  if (!in_range(a, c.num_pages) || !in_range(b, c.num_pages) || a == b) return;
+  const int64_t at = pool * c.pool_stride + (int64_t)span * kCopyBytes;
+  copy_span(c.pool + at + a * c.page_stride, c.pool + at + b * c.page_stride, page_bytes - (int64_t)span * kCopyBytes);
+}
+
+// ---------------------------------------------------------------- fork
+// Workspace of a fork: the sources' rows as they were before the call, then
+// their lengths and the page each entry was given.
+struct ForkSpace {
+  int32_t* rows;   // [n][max_pages]
+  int32_t* len;    // [n]
+  int32_t* fresh;  // [n]: a page, -1: none needed, -2: not served, -3: bad entry
+};
+constexpr int kNone = -1, kUnserved = -2, kBadEntry = -3;
+
+__device__ __forceinline__ bool fork_entry_good(const PageView& c, int32_t s, int32_t d) {
+  if (!in_range(s, c.max_seqs) || !in_range(d, c.max_seqs)) return false;
+  const int32_t len = c.seq_len[s];
+  return len >= 0 && pages_of(len, c.page_size) <= c.max_pages;
+}
+
+// Block 0 gives out the pages; block 1 + i saves the row of src[i] and counts
+// dst[i] as an owner of its full pages.  The counts that block 0 looks for are
+// zeros, those that the other blocks raise are not.
+__global__ void __launch_bounds__(kScanThreads) fork_plan_kernel(PageView c, const int32_t* __restrict__ src,
+                                                                 const int32_t* __restrict__ dst, int n,
+                                                                 ForkSpace ws, int32_t* __restrict__ status) {
+  if (blockIdx.x > 0) {
+    const int i = blockIdx.x - 1;
+    if (repeated(dst, i) || !fork_entry_good(c, src[i], dst[i])) return;
+    const int32_t s = src[i], len = c.seq_len[s];
+    const int full = len / c.page_size, used = (int)pages_of(len, c.page_size);
+    if (threadIdx.x == 0) ws.len[i] = len;
+    for (int w = threadIdx.x; w < used; w += kScanThreads) {
+      const int32_t p = c.table[(int64_t)s * c.ld_table + w];
+      ws.rows[(int64_t)i * c.max_pages + w] = p;
+      if (w < full && in_range(p, c.num_pages)) atomicAdd(&c.refs[p], 1);
+    }
+    return;
+  }
+  __shared__ int scratch[kScanThreads / kWave + 1];
+  __shared__ int32_t ids[kMaxPageEntries];
+  __shared__ int32_t who[kMaxPageEntries];  // entry of the rank-th page
+  const int tid = threadIdx.x;
+  for (int i = tid; i < n; i += kScanThreads) ids[i] = dst[i];
+  __syncthreads();
+  int total = 0;
+  for (int base = 0; base < n; base += kScanThreads) {
+    const int i = base + tid;
+    int need = 0;
+    if (i < n) {
+      bool good = fork_entry_good(c, src[i], ids[i]);
+      for (int j = 0; j < i; ++j) good &= ids[j] != ids[i];
+      need = good && c.seq_len[src[i]] % c.page_size != 0;
+      if (!need) {
+        ws.fresh[i] = good ? kNone : kBadEntry;
+        if (status) status[i] = good ? kOk : kBad;
+      }
+    }
+    int sum;
+    const int excl = block_exclusive_sum<kScanThreads>(need, scratch, &sum);
+    if (need) who[total + excl] = i;
+    total += sum;
+  }
+  __syncthreads();
+  const int found = scan_free(c.refs, c.num_pages, total, scratch, [&](int rank, int32_t page) {
+    const int i = who[rank];
+    ws.fresh[i] = page;
+    c.refs[page] = 1;
+    if (status) status[i] = kOk;
+  });
+  for (int r = found + tid; r < total; r += kScanThreads) {
+    ws.fresh[who[r]] = kUnserved;
+    if (status) status[who[r]] = kNoSpace;
+  }
+}
+
+// Blocks (i, 0) rewrite the row of dst[i]; blocks (i, 1 + pool) copy the
+// filled rows of the last page.
+__global__ void __launch_bounds__(256) fork_move_kernel(PageView c, const int32_t* __restrict__ dst, ForkSpace ws) {
+  const int i = blockIdx.x;
+  const int32_t fresh = ws.fresh[i];
+  if (fresh == kBadEntry) return;
+  const int32_t len = ws.len[i];
+  const int full = len / c.page_size, rest = len % c.page_size;
+  const int32_t* saved = ws.rows + (int64_t)i * c.max_pages;
+  if (blockIdx.y == 0) {
+    int32_t* row = c.table + (int64_t)dst[i] * c.ld_table;
+    if (fresh == kUnserved) {  // dst keeps its state: it is no owner of src's pages
+      for (int w = threadIdx.x; w < full; w += 256)
+        if (in_range(saved[w], c.num_pages)) atomicSub(&c.refs[saved[w]], 1);
+      return;
+    }
+    for (int w = threadIdx.x; w < c.max_pages; w += 256) {
+      const int32_t old = row[w];
+      if (in_range(old, c.num_pages)) atomicSub(&c.refs[old], 1);
+      row[w] = w < full ? saved[w] : w == full && fresh >= 0 ? fresh : -1;
+    }
+    if (threadIdx.x == 0) c.seq_len[dst[i]] = len;
+    return;
+  }
+  if (fresh < 0) return;
+  const int32_t last = saved[full];
+  if (!in_range(last, c.num_pages)) return;
+  const int64_t pool = blockIdx.y - 1;
+  const int64_t bytes = rest * c.row_bytes, chunk = c.page_size * c.row_bytes;
+  const uint8_t* from = c.pool + pool * c.pool_stride + last * c.page_stride;
+  uint8_t* to = c.pool + pool * c.pool_stride + fresh * c.page_stride;
+  for (int h = 0; h < c.chunks; ++h)
+    for (int64_t at = 0; at < bytes; at += kCopyBytes)
+      copy_span(from + h * chunk + at, to + h * chunk + at, bytes - at);
+}
+
+// ---------------------------------------------------------------- free
+__global__ void __launch_bounds__(256) free_kernel(PageView c, const int32_t* __restrict__ seqs) {
+  const int i = blockIdx.x;
+  const int32_t s = seqs[i];
+  if (repeated(seqs, i) || !in_range(s, c.max_seqs)) return;
+  int32_t* row = c.table + (int64_t)s * c.ld_table;
+  for (int w = threadIdx.x; w < c.max_pages; w += 256) {
+    const int32_t p = row[w];
+    if (in_range(p, c.num_pages)) atomicSub(&c.refs[p], 1);
+    row[w] = -1;
+  }
+  if (threadIdx.x == 0) c.seq_len[s] = 0;
+}
+
+// ---------------------------------------------------------------- append
+__global__ void __launch_bounds__(256) append_kernel(PageView c, AppendArgs a) {
+  const int t = blockIdx.x;
+  // The sequence of token t: the last i with start[i] <= t.
+  int lo = 0, hi = a.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (a.start[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const int32_t s = a.seqs[lo];
+  if (!in_range(s, c.max_seqs)) return;
+  const int64_t pos = (int64_t)c.seq_len[s] + t - a.start[lo];
+  if (pos < 0 || t < a.start[lo] || t >= a.start[lo + 1]) return;
+  const int64_t w = pos / c.page_size;
+  if (w >= c.max_pages) return;
+  const int32_t page = c.table[(int64_t)s * c.ld_table + w];
+  if (!in_range(page, c.num_pages)) return;
+  const int pieces = a.dim / 8;
+  const int64_t slot = pos % c.page_size;
+  const int64_t chunk_bytes = c.page_size * c.row_bytes;
+  const int64_t at = page * c.page_stride + slot * c.row_bytes;
+  for (int e = threadIdx.x; e < a.heads * pieces; e += 256) {
+    const int h = e / pieces, d = e % pieces * 8;
+    const int64_t in_page = c.chunks == 1 ? ((int64_t)h * a.dim + d) * 2 : h * chunk_bytes + d * 2;
+    *reinterpret_cast<u32x4*>(c.pool + a.k_pool * c.pool_stride + at + in_page) =
+        *reinterpret_cast<const u32x4*>(a.k + t * a.k_token + h * a.k_head + d);
+    *reinterpret_cast<u32x4*>(c.pool + a.v_pool * c.pool_stride + at + in_page) =
+        *reinterpret_cast<const u32x4*>(a.v + t * a.v_token + h * a.v_head + d);
+  }
+}
+
+// ---------------------------------------------------------------- accept
+// Block (i, pool).  A lane owns 16 bytes of a row and moves them for j = 0, 1,
+// ... in order: row j is written after row path[j] >= j was read, and every
+// later read is of a row above j, so no row is overwritten before it is read.
+constexpr int kAcceptUnroll = 4;
+
+__global__ void __launch_bounds__(256) accept_kernel(PageView c, const int32_t* __restrict__ seqs,
+                                                     const int32_t* __restrict__ drafted,
+                                                     const int32_t* __restrict__ path, int64_t ld_path, int columns,
+                                                     const int32_t* __restrict__ accepted,
+                                                     int32_t* __restrict__ new_len) {
+  __shared__ int64_t from[kMaxPath], to[kMaxPath];  // byte offsets in a pool; from < 0: nothing to move
+  __shared__ int ends;
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int32_t s = seqs[i];
+  if (!in_range(s, c.max_seqs)) {
+    if (blockIdx.y == 0 && tid == 0) new_len[i] = 0;
+    return;
+  }
+  const int32_t len = c.seq_len[s];
+  const int most = min(max(accepted[i], 0), columns);
+  if (tid == 0) ends = most;
+  __syncthreads();
+  const int32_t* mine = path + (int64_t)i * ld_path;
+  if (tid < most) {
+    const int32_t p = mine[tid], before = tid ? mine[tid - 1] : -1;
+    if (p <= before || p >= drafted[i]) atomicMin(&ends, tid);
+  }
+  __syncthreads();
+  const int kept = ends;
+  if (blockIdx.y == 0 && tid == 0) new_len[i] = len + kept;
+  if (tid < kept) {
+    const int32_t p = mine[tid];
+    int64_t f = -1, t = -1;
+    const int64_t fp = ((int64_t)len + p) / c.page_size, tp = ((int64_t)len + tid) / c.page_size;
+    if (p != tid && len >= 0 && fp < c.max_pages) {
+      const int32_t a = c.table[(int64_t)s * c.ld_table + fp], b = c.table[(int64_t)s * c.ld_table + tp];
+      if (in_range(a, c.num_pages) && in_range(b, c.num_pages)) {
+        f = a * c.page_stride + ((int64_t)len + p) % c.page_size * c.row_bytes;
+        t = b * c.page_stride + ((int64_t)len + tid) % c.page_size * c.row_bytes;
+      }
+    }
+    from[tid] = f;
+    to[tid] = t;
+  }
+  __syncthreads();
+  uint8_t* pool = c.pool + (int64_t)blockIdx.y * c.pool_stride;
+  const int64_t chunk = c.page_size * c.row_bytes;
+  const int pieces = (int)(c.row_bytes / 16);
+  for (int64_t e = tid; e < (int64_t)pieces * c.chunks; e += 256) {
+    uint8_t* at = pool + e / pieces * chunk + e % pieces * 16;
+    for (int j0 = 0; j0 < kept; j0 += kAcceptUnroll) {
+      u32x4 v[kAcceptUnroll];
+#pragma unroll
+      for (int u = 0; u < kAcceptUnroll; ++u)
+        if (j0 + u < kept && from[j0 + u] >= 0) v[u] = *reinterpret_cast<const u32x4*>(at + from[j0 + u]);
+#pragma unroll
+      for (int u = 0; u < kAcceptUnroll; ++u)
+        if (j0 + u < kept && from[j0 + u] >= 0) *reinterpret_cast<u32x4*>(at + to[j0 + u]) = v[u];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- compact
+// Workspace: the pages that move and where to, their number, and the new id of
+// every page.
+struct CompactSpace {
+  int32_t* from;   // [num_pages]
+  int32_t* to;     // [num_pages]
+  int32_t* now;    // [num_pages]
+  int32_t* moves;  // [1]
+};
+
+__global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(PageView c, CompactSpace ws,
+                                                                    int32_t* __restrict__ live_out) {
+  __shared__ int scratch[kScanThreads / kWave + 1];
+  const int tid = threadIdx.x;
+  int live = 0;
+  for (int64_t base = 0; base < c.num_pages; base += kScanThreads) {
+    const int64_t p = base + tid;
+    int sum;
+    block_exclusive_sum<kScanThreads>(p < c.num_pages && c.refs[p] != 0, scratch, &sum);
+    live += sum;
+  }
+  // Free pages below `live` and live pages at or above it are equally many.
+  int holes = 0, moving = 0;
+  for (int64_t base = 0; base < c.num_pages; base += kScanThreads) {
+    const int64_t p = base + tid;
+    const bool in = p < c.num_pages;
+    const bool used = in && c.refs[p] != 0;
+    const bool hole = in && p < live && !used, moves = used && p >= live;
+    int sum;
+    int rank = block_exclusive_sum<kScanThreads>(hole, scratch, &sum);
+    if (hole) ws.to[holes + rank] = (int32_t)p;
+    holes += sum;
+    rank = block_exclusive_sum<kScanThreads>(moves, scratch, &sum);
+    if (moves) ws.from[moving + rank] = (int32_t)p;
+    moving += sum;
+    if (in) ws.now[p] = (int32_t)p;
+  }
+  __syncthreads();
+  for (int i = tid; i < moving; i += kScanThreads) {
+    const int32_t a = ws.from[i], b = ws.to[i];
+    ws.now[a] = b;
+    c.refs[b] = c.refs[a];
+    c.refs[a] = 0;
+  }
+  if (tid == 0) {
+    *ws.moves = moving;
+    *live_out = live;
+  }
+}
+
+// Every block takes (move, pool, span) items in turn: the number of moves is
+// known on the device only.
+__global__ void __launch_bounds__(256) compact_copy_kernel(PageView c, CompactSpace ws, int64_t page_bytes, int spans) {
+  const int64_t items = (int64_t)*ws.moves * c.num_pools * spans;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int span = (int)(it % spans);
+    const int64_t pool = it / spans % c.num_pools;
+    const int64_t i = it / spans / c.num_pools;
+    const int64_t at = pool * c.pool_stride + (int64_t)span * kCopyBytes;
+    copy_span(c.pool + at + ws.from[i] * c.page_stride, c.pool + at + ws.to[i] * c.page_stride,
+              page_bytes - (int64_t)span * kCopyBytes);
+  }
+}
+
+__global__ void __launch_bounds__(256) compact_table_kernel(PageView c, CompactSpace ws) {
+  int32_t* row = c.table + (int64_t)blockIdx.x * c.ld_table;
+  for (int w = threadIdx.x; w < c.max_pages; w += 256) {
+    const int32_t p = row[w];
+    if (in_range(p, c.num_pages)) row[w] = ws.now[p];
+  }
+}
+
+int64_t page_bytes_of(const PageView& c) { return (int64_t)c.chunks * c.page_size * c.row_bytes; }
+int spans_of(const PageView& c) { return (int)((page_bytes_of(c) + kCopyBytes - 1) / kCopyBytes); }
+
+ForkSpace fork_space(void* ws, int32_t n, int32_t max_pages) {
+  ForkSpace f;
+  f.len = static_cast<int32_t*>(ws);
+  f.fresh = f.len + n;
+  f.rows = f.fresh + n;
+  return f;
+}
+
+}  // namespace
+
+size_t fork_workspace(int32_t n, int32_t max_pages) { return ((size_t)n * (size_t)max_pages + 2 * (size_t)n) * 4; }
+size_t compact_workspace(int32_t num_pages) { return 3 * (size_t)num_pages * 4 + 16; }
+
+hipError_t launch_pages_resize(const PageView& c, const int32_t* seqs, const int32_t* lens, const int32_t* extra,
+                               int32_t n, int32_t* status, hipStream_t s) {
+  resize_kernel<<<1, kScanThreads, 0, s>>>(c, seqs, lens, extra, n, status);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_copy(const PageView& c, const int32_t* src, const int32_t* dst, int32_t n, hipStream_t s) {
+  const int spans = spans_of(c);
+  copy_kernel<<<dim3((unsigned)(spans * c.num_pools), n), 256, 0, s>>>(c, src, dst, page_bytes_of(c), spans);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_fork(const PageView& c, const int32_t* src, const int32_t* dst, int32_t n, int32_t* status,
+                             void* workspace, hipStream_t s) {
+  const ForkSpace ws = fork_space(workspace, n, c.max_pages);
+  fork_plan_kernel<<<1 + n, kScanThreads, 0, s>>>(c, src, dst, n, ws, status);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  fork_move_kernel<<<dim3(n, 1 + c.num_pools), 256, 0, s>>>(c, dst, ws);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_free(const PageView& c, const int32_t* seqs, int32_t n, hipStream_t s) {
+  free_kernel<<<n, 256, 0, s>>>(c, seqs);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_append(const PageView& c, const AppendArgs& a, int32_t T, hipStream_t s) {
+  append_kernel<<<T, 256, 0, s>>>(c, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_accept(const PageView& c, const int32_t* seqs, const int32_t* drafted, const int32_t* path,
+                               int64_t ld_path, int32_t columns, const int32_t* accepted, int32_t n, int32_t* new_len,
+                               hipStream_t s) {
+  accept_kernel<<<dim3(n, c.num_pools), 256, 0, s>>>(c, seqs, drafted, path, ld_path, columns, accepted, new_len);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_compact(const PageView& c, int32_t* live, void* workspace, hipStream_t s) {
+  CompactSpace ws;
+  ws.moves = static_cast<int32_t*>(workspace);
+  ws.from = ws.moves + 4;
+  ws.to = ws.from + c.num_pages;
+  ws.now = ws.to + c.num_pages;
+  compact_plan_kernel<<<1, kScanThreads, 0, s>>>(c, ws, live);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  compact_copy_kernel<<<2048, 256, 0, s>>>(c, ws, page_bytes_of(c), spans_of(c));
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  compact_table_kernel<<<c.max_seqs, 256, 0, s>>>(c, ws);
+  return hipGetLastError();
+}
+
+}  // namespace lora

@@ -1,0 +1,396 @@
+"""Python binding of the decode-step operators of liblora_mi355x
+(``include/lora_decode.h``): 4-bit base products, attention of drafted tokens
+over a paged cache, and the cache's page operations.
+
+Argument marshalling only, as in the package's ``__init__``: shapes, strides,
+dtype codes and the current stream of torch tensors.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import lora_serving_build_amd as _base
+
+__all__ = [
+    "Q4Weight", "lora_q4_packed_bytes", "lora_q4_pack", "lora_q4_matmul",
+    "lora_tree_attention", "lora_tree_attention_workspace_bytes",
+    "PageCache", "lora_pages_resize", "lora_pages_append", "lora_pages_copy", "lora_pages_fork",
+    "lora_pages_fork_workspace_bytes", "lora_pages_accept", "lora_pages_free", "lora_pages_compact",
+    "lora_pages_compact_workspace_bytes", "PAGES_OK", "PAGES_NO_SPACE", "PAGES_BAD",
+    "LORA_MAX_PAGE_ENTRIES", "LORA_MAX_PATH", "LORA_MAX_HEAD_DIM",
+]
+
+PAGES_OK, PAGES_NO_SPACE, PAGES_BAD = 0, 1, 2
+LORA_MAX_PAGE_ENTRIES, LORA_MAX_PATH, LORA_MAX_HEAD_DIM = 2048, 256, 256
+
+_DTYPE = {torch.float16: 0, torch.bfloat16: 1}
+
+
+class _CQ4Weight(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("has_zeros", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("packed", ctypes.c_void_p),
+    ]
+
+
+class _CTreeBatch(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("start", ctypes.c_void_p),
+        ("ctx_len", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("mask", ctypes.c_void_p),
+        ("ld_mask", ctypes.c_int64),
+        ("mask_words", ctypes.c_int32),
+    ]
+
+
+class _CKvLayer(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+    ]
+
+
+class _CPageCache(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p),
+        ("pool_stride", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("row_bytes", ctypes.c_int64),
+        ("chunks", ctypes.c_int32),
+        ("num_pools", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("refs", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("max_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("seq_len", ctypes.c_void_p),
+    ]
+
+
+def _declare(L) -> None:
+    p, i32, i64, sz, ci = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    L.lora_q4_packed_bytes.argtypes = [i32, i32, i32, ci]
+    L.lora_q4_packed_bytes.restype = sz
+    L.lora_q4_pack.argtypes = [p, i64, p, i64, p, i64, i32, i32, i32, ci, p, sz, p, p]
+    L.lora_q4_matmul.argtypes = [p, i64, p, i32, p, i64, ci, p]
+    L.lora_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.lora_tree_attention_workspace_bytes.restype = sz
+    L.lora_tree_attention.argtypes = [p, i64, i64, p, p, i32, i32, i32, ctypes.c_float, p, i64, i64, p, p, sz, ci, p]
+    L.lora_pages_resize.argtypes = [p, p, p, p, i32, p, p]
+    L.lora_pages_append.argtypes = [p, i32, i32, p, i64, i64, p, i64, i64, i32, i32, p, p, i32, i32, p]
+    L.lora_pages_copy.argtypes = [p, p, p, i32, p]
+    L.lora_pages_fork_workspace_bytes.argtypes = [i32, i32]
+    L.lora_pages_fork_workspace_bytes.restype = sz
+    L.lora_pages_fork.argtypes = [p, p, p, i32, p, p, sz, p]
+    L.lora_pages_accept.argtypes = [p, p, p, p, i64, i32, p, i32, p, p]
+    L.lora_pages_free.argtypes = [p, p, i32, p]
+    L.lora_pages_compact_workspace_bytes.argtypes = [i32]
+    L.lora_pages_compact_workspace_bytes.restype = sz
+    L.lora_pages_compact.argtypes = [p, p, p, sz, p]
+    for f in ("lora_q4_pack", "lora_q4_matmul", "lora_tree_attention", "lora_pages_resize", "lora_pages_append",
+              "lora_pages_copy", "lora_pages_fork", "lora_pages_accept", "lora_pages_free", "lora_pages_compact"):
+        getattr(L, f).restype = ci
+
+
+def _run(rc: int) -> None:
+    if rc:
+        raise _base.LoraError(rc, _base.lora_last_error())
+
+
+def _stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}: {name} must be float16 or bfloat16")
+    return code
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D device tensor with contiguous rows."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _on_gpu(device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device != device):
+            raise ValueError("every tensor must be on the same GPU")
+
+
+# ---------------------------------------------------------------- 4-bit products
+class Q4Weight:
+    """A weight in the kernel's layout: the packed device buffer and the C
+    struct that points at it."""
+
+    def __init__(self, packed: torch.Tensor, n: int, k: int, group: int, has_zeros: bool, dtype: torch.dtype):
+        self.packed, self.n, self.k, self.group, self.has_zeros, self.dtype = packed, n, k, group, has_zeros, dtype
+        self.c = _CQ4Weight(n, k, group, int(has_zeros), _DTYPE[dtype], packed.data_ptr())
+        self._ref = ctypes.addressof(self.c)
+
+
+def lora_q4_packed_bytes(n: int, k: int, group: int, has_zeros: bool) -> int:
+    return int(_base.lib().lora_q4_packed_bytes(int(n), int(k), int(group), int(bool(has_zeros))))
+
+
+def lora_q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None, k: int,
+                 group: int) -> Q4Weight:
+    """Lays a weight out for lora_q4_matmul.  codes: uint8 [n][ceil(k / 2)],
+    input 2 i in the low half of byte i; scales: float16 or bfloat16
+    [n][ceil(k / group)]; zeros: uint8 of the scales' shape, or None (8)."""
+    code = _code(scales, "scales")
+    if codes.dtype != torch.uint8 or (zeros is not None and zeros.dtype != torch.uint8):
+        raise TypeError("codes and zeros must be uint8")
+    ldc, lds = _rows(codes, "codes"), _rows(scales, "scales")
+    ldz = _rows(zeros, "zeros") if zeros is not None else 0
+    n, k, group = codes.shape[0], int(k), int(group)
+    groups = -(-k // group) if group > 0 else 0
+    if codes.shape[1] < (k + 1) // 2 or scales.shape[0] != n or scales.shape[1] < groups:
+        raise ValueError("codes must be [n][ceil(k / 2)] and scales [n][ceil(k / group)]")
+    if zeros is not None and (zeros.shape[0] != n or zeros.shape[1] < groups):
+        raise ValueError("zeros must have the scales' shape")
+    need = lora_q4_packed_bytes(n, k, group, zeros is not None)
+    packed = torch.empty(max(need, 16), dtype=torch.uint8, device=codes.device)
+    w = Q4Weight(packed, n, k, group, zeros is not None, scales.dtype)
+    if need:  # a shape without a packed form is refused below, before any launch
+        _on_gpu(codes.device, codes, scales, zeros)
+    stream = _stream(codes) if codes.is_cuda else 0
+    _run(_base.lib().lora_q4_pack(codes.data_ptr(), ldc, scales.data_ptr(), lds,
+                                  zeros.data_ptr() if zeros is not None else None, ldz, n, k, group, code,
+                                  packed.data_ptr(), packed.numel(), w._ref, stream))
+    return w
+
+
+def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bool = False) -> torch.Tensor:
+    """y[t, :n] (+)= x[t, :k] . W for every row t of x (decode and
+    verification batches); y is [T][n] in the weight's dtype, and is returned."""
+    if x.dtype != w.dtype or y.dtype != w.dtype:
+        raise TypeError("x and y must have the weight's dtype")
+    ldx, ldy = _rows(x, "x"), _rows(y, "y")
+    T = x.shape[0]
+    if x.shape[1] != w.k or y.shape[1] != w.n or y.shape[0] < T:
+        raise ValueError(f"x must be [T][{w.k}] and y [T][{w.n}]")
+    _on_gpu(w.packed.device, x, y)
+    _run(_base.lib().lora_q4_matmul(x.data_ptr(), ldx, w._ref, T, y.data_ptr(), ldy, int(add_inputs), _stream(x)))
+    return y
+
+
+# ---------------------------------------------------------------- tree attention
+def _int32(t: torch.Tensor, name: str, n: int | None = None) -> int:
+    """Address of a contiguous int32 vector of (at least) n entries."""
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] < n):
+        raise ValueError(f"{name} must be a contiguous int32 vector" + (f" of {n} entries" if n is not None else ""))
+    return t.data_ptr()
+
+
+def _workspace(t: torch.Tensor, nbytes: int, given: torch.Tensor | None):
+    ws = _base._workspace(t.device, nbytes) if given is None else given
+    return (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
+
+
+def lora_tree_attention_workspace_bytes(B: int, T: int, heads: int, kv_heads: int, dim: int) -> int:
+    return int(_base.lib().lora_tree_attention_workspace_bytes(B, T, heads, kv_heads, dim))
+
+
+def lora_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                        ctx_len: torch.Tensor, start: torch.Tensor, out: torch.Tensor, scale: float,
+                        mask: torch.Tensor | None = None, lse: torch.Tensor | None = None, head_major: bool = False,
+                        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of each sequence's drafted tokens over its cached positions.
+
+    q, out [T][heads][dim]; k_cache, v_cache [num_pages][page_size][kv_heads][dim]
+    (head_major: [num_pages][kv_heads][page_size][dim]) with the drafted tokens'
+    keys and values already in place; table int32 [B][max_pages]; ctx_len int32
+    [B]; start int32 [B + 1]; mask int64 [T][words], bit j of a row: the row sees
+    node j of its sequence (None: node i sees nodes 0..i); lse float32
+    [T][heads].  Returns out."""
+    code = _code(q, "q")
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype:
+        raise TypeError("q, k_cache, v_cache and out must share a dtype")
+    if q.dim() != 3 or k_cache.dim() != 4 or out.shape != q.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("q and out must be [T][heads][dim], k_cache and v_cache four-dimensional and alike")
+    T, heads, dim = q.shape
+    num_pages, page_size, kv_heads, kdim = k_cache.shape
+    page_st, token_st, head_st, one = k_cache.stride()
+    if head_major:
+        page_size, kv_heads, token_st, head_st = kv_heads, page_size, head_st, token_st
+    if kdim != dim or one != 1 or v_cache.stride() != k_cache.stride() or q.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("head dims must agree and be contiguous, k_cache and v_cache must have the same strides")
+    if table.dtype != torch.int32 or table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError("table must be an int32 [B][max_pages] tensor with contiguous rows")
+    B, max_pages = table.shape
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [T][heads] tensor")
+    words, ld_mask, mask_ptr = 0, 0, None
+    if mask is not None:
+        if mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] < T or (mask.stride(1) != 1 and mask.shape[1] > 1):
+            raise ValueError("mask must be an int64 [T][words] tensor with contiguous rows")
+        words, mask_ptr = mask.shape[1], mask.data_ptr()
+        ld_mask = max(mask.stride(0), words)
+    _on_gpu(q.device, q, k_cache, v_cache, table, ctx_len, start, out, mask, lse, workspace)
+    batch = _CTreeBatch(B, T, _int32(start, "start", B + 1), _int32(ctx_len, "ctx_len", B), table.data_ptr(),
+                        max(table.stride(0), max_pages), max_pages, mask_ptr, ld_mask, words)
+    layer = _CKvLayer(k_cache.data_ptr(), v_cache.data_ptr(), page_st, token_st, head_st, num_pages, page_size)
+    L = _base.lib()
+    ws, ws_bytes = _workspace(q, L.lora_tree_attention_workspace_bytes(B, T, heads, kv_heads, dim), workspace)
+    _run(L.lora_tree_attention(q.data_ptr(), q.stride(0), q.stride(1), ctypes.addressof(layer),
+                               ctypes.addressof(batch), heads, kv_heads, dim, scale, out.data_ptr(), out.stride(0),
+                               out.stride(1), lse.data_ptr() if lse is not None else None, ws, ws_bytes, code,
+                               _stream(q)))
+    return out
+
+
+# ---------------------------------------------------------------- pages
+class PageCache:
+    """A paged cache: its device buffers and the C struct that points at them.
+
+    pool     [num_pools][num_pages][page_size][heads][dim] of a 16-bit type
+             (head_major: [num_pools][num_pages][heads][page_size][dim]), pages
+             contiguous; one pool for each layer's keys and one for its values
+    refs     int32 [num_pages] reference counts, 0 = free
+    table    int32 [max_seqs][max_pages] page ids, -1 behind a row's last page
+    seq_len  int32 [max_seqs] cached tokens
+
+    A new cache has zeros in refs and seq_len and -1 throughout table."""
+
+    def __init__(self, pool: torch.Tensor, refs: torch.Tensor, table: torch.Tensor, seq_len: torch.Tensor,
+                 head_major: bool = False):
+        if pool.dim() != 5 or pool.element_size() != 2 or not pool[0, 0].is_contiguous():
+            raise ValueError("pool must be a five-dimensional tensor of a 16-bit type with contiguous pages")
+        if table.dtype != torch.int32 or table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
+            raise ValueError("table must be an int32 [max_seqs][max_pages] tensor with contiguous rows")
+        pools, pages, a, b, dim = pool.shape
+        self.page_size, self.heads, self.dim, self.head_major = (b, a, dim, True) if head_major else (a, b, dim, False)
+        max_seqs, max_pages = table.shape
+        refs_ptr, len_ptr = _int32(refs, "refs", pages), _int32(seq_len, "seq_len", max_seqs)
+        _on_gpu(pool.device, pool, refs, table, seq_len)
+        self.pool, self.refs, self.table, self.seq_len = pool, refs, table, seq_len
+        self.num_pages, self.max_pages = pages, max_pages
+        self.c = _CPageCache(pool.data_ptr(), pool.stride(0) * 2, pool.stride(1) * 2,
+                             dim * 2 if head_major else b * dim * 2, a if head_major else 1, pools, pages,
+                             self.page_size, refs_ptr, table.data_ptr(), max(table.stride(0), max_pages), max_seqs,
+                             max_pages, len_ptr)
+        self._ref = ctypes.addressof(self.c)
+
+    def layer(self, i: int):
+        """Keys and values of layer i (pools 2 i and 2 i + 1), as
+        lora_tree_attention takes them."""
+        return self.pool[2 * i], self.pool[2 * i + 1]
+
+
+def _entries(cache: PageCache, n: int | None, **vectors):
+    """Number of entries and the addresses of the int32 vectors (None stays)."""
+    out = []
+    for name, t in vectors.items():
+        if t is None:
+            out.append(None)
+            continue
+        if n is None:
+            n = t.shape[0] if t.dim() == 1 else -1
+        out.append(_int32(t, name, n))
+        if t.device != cache.pool.device:
+            raise ValueError("every tensor must be on the cache's GPU")
+    return n, *out
+
+
+def lora_pages_resize(cache: PageCache, seqs: torch.Tensor, lens: torch.Tensor | None = None,
+                      extra: torch.Tensor | None = None, status: torch.Tensor | None = None) -> None:
+    """Sets the sequences' lengths (lens; None: as they are) and makes their
+    rows hold exactly the pages of length + extra tokens.  status (optional):
+    PAGES_OK, PAGES_NO_SPACE or PAGES_BAD for each."""
+    n, ps, pl, pe, pt = _entries(cache, None, seqs=seqs, lens=lens, extra=extra, status=status)
+    _run(_base.lib().lora_pages_resize(cache._ref, ps, pl, pe, n, pt, _stream(seqs)))
+
+
+def lora_pages_append(cache: PageCache, layer: int, k: torch.Tensor, v: torch.Tensor, seqs: torch.Tensor,
+                      start: torch.Tensor) -> None:
+    """Stores new tokens' keys and values ([T][heads][dim] each) of one layer
+    behind the sequences' cached tokens: rows start[i] .. start[i + 1] - 1 go to
+    positions seq_len[seqs[i]] and on."""
+    if k.dtype != cache.pool.dtype or v.dtype != cache.pool.dtype:
+        raise TypeError("k and v must have the cache's dtype")
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (cache.heads, cache.dim) or k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v must be [T][heads][dim] with contiguous head dims, as in the cache")
+    n = seqs.shape[0]
+    _, ps = _entries(cache, n, seqs=seqs)
+    _, pst = _entries(cache, n + 1, start=start)
+    _on_gpu(cache.pool.device, k, v)
+    _run(_base.lib().lora_pages_append(cache._ref, 2 * layer, 2 * layer + 1, k.data_ptr(), k.stride(0), k.stride(1),
+                                       v.data_ptr(), v.stride(0), v.stride(1), cache.heads, cache.dim, ps, pst, n,
+                                       k.shape[0], _stream(k)))
+
+
+def lora_pages_copy(cache: PageCache, src_pages: torch.Tensor, dst_pages: torch.Tensor) -> None:
+    """Copies page src_pages[i] to page dst_pages[i] in every pool."""
+    n, ps, pd = _entries(cache, None, src_pages=src_pages, dst_pages=dst_pages)
+    _run(_base.lib().lora_pages_copy(cache._ref, ps, pd, n, _stream(src_pages)))
+
+
+def lora_pages_fork_workspace_bytes(n: int, max_pages: int) -> int:
+    return int(_base.lib().lora_pages_fork_workspace_bytes(n, max_pages))
+
+
+def lora_pages_fork(cache: PageCache, src: torch.Tensor, dst: torch.Tensor, status: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> None:
+    """Gives every sequence dst[i] the state that src[i] had before the call:
+    full pages are shared, the last, partly filled one is copied, and what
+    dst[i] held is released."""
+    n, ps, pd, pt = _entries(cache, None, src=src, dst=dst, status=status)
+    L = _base.lib()
+    ws, ws_bytes = _workspace(src, L.lora_pages_fork_workspace_bytes(n, cache.max_pages), workspace)
+    _run(L.lora_pages_fork(cache._ref, ps, pd, n, pt, ws, ws_bytes, _stream(src)))
+
+
+def lora_pages_accept(cache: PageCache, seqs: torch.Tensor, drafted: torch.Tensor, path: torch.Tensor,
+                      accepted: torch.Tensor, new_len: torch.Tensor) -> torch.Tensor:
+    """Moves the accepted nodes' rows (path int32 [n][columns], accepted[i] of
+    them) to the front of each sequence's drafted rows, in every pool.  new_len
+    receives seq_len + the rows kept; a resize with it makes that the length."""
+    n, ps, pd, pa, pn = _entries(cache, None, seqs=seqs, drafted=drafted, accepted=accepted, new_len=new_len)
+    if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] < n or (path.stride(1) != 1 and path.shape[1] > 1):
+        raise ValueError("path must be an int32 [n][columns] tensor with contiguous rows")
+    _on_gpu(cache.pool.device, path)
+    _run(_base.lib().lora_pages_accept(cache._ref, ps, pd, path.data_ptr(), max(path.stride(0), path.shape[1]),
+                                       path.shape[1], pa, n, pn, _stream(seqs)))
+    return new_len
+
+
+def lora_pages_free(cache: PageCache, seqs: torch.Tensor) -> None:
+    """Releases every page of the sequences."""
+    n, ps = _entries(cache, None, seqs=seqs)
+    _run(_base.lib().lora_pages_free(cache._ref, ps, n, _stream(seqs)))
+
+
+def lora_pages_compact_workspace_bytes(num_pages: int) -> int:
+    return int(_base.lib().lora_pages_compact_workspace_bytes(num_pages))
+
+
+def lora_pages_compact(cache: PageCache, live: torch.Tensor, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Moves the live pages to the lowest ids, in every pool and table row;
+    live[0] receives their number."""
+    _, pl = _entries(cache, 1, live=live)
+    L = _base.lib()
+    ws, ws_bytes = _workspace(live, L.lora_pages_compact_workspace_bytes(cache.num_pages), workspace)
+    _run(L.lora_pages_compact(cache._ref, pl, ws, ws_bytes, _stream(live)))
+    return live
