@@ -62,13 +62,13 @@ __device__ __forceinline__ Space space(const AttnArgs& a) {
 }
 
 __device__ __forceinline__ int row_tiles(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
-__device__ __forceinline__ int key_tiles(int len) { return max((len + kTile - 1) / kTile, 1); }
+__device__ __forceinline__ int key_tiles(int len, int keys) { return max((len + keys - 1) / keys, 1); }
 
 // Item number `work`; false if there are fewer.  Items of a sequence: (run,
 // head) units in groups of eight, the row tiles of a group's units one after
 // the other, so that the row tiles that read the same keys are eight workgroups
 // apart and share an XCD's L2.
-template <int ROWS>
+template <int ROWS, int KEYS>
 __device__ __forceinline__ bool find_item(const AttnArgs& a, int work, int slots, Item* it) {
   const int lane = threadIdx.x & (kWave - 1);
   const int group = a.heads / a.kv_heads;
@@ -77,7 +77,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, int work, int slots
     int mine = 0;
     if (base + lane < a.B) {
       const Seq s = sequence(a, base + lane);
-      mine = row_tiles(s.n, group, ROWS) * key_tiles(s.len) * a.kv_heads;
+      mine = row_tiles(s.n, group, ROWS) * key_tiles(s.len, KEYS) * a.kv_heads;
     }
     units += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(mine), kWave - 1);
   }
@@ -91,7 +91,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, int work, int slots
     if (base + lane < a.B) {
       s = sequence(a, base + lane);
       rts = row_tiles(s.n, group, ROWS);
-      splits = (key_tiles(s.len) + tiles - 1) / tiles;
+      splits = (key_tiles(s.len, KEYS) + tiles - 1) / tiles;
     }
     const int count = rts * splits * a.kv_heads, cut = splits > 1 ? count : 0;
     const int end = before + wave_inclusive_sum(count);
@@ -132,15 +132,18 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, int work, int slots
   return found;
 }
 
-// Floats of one slot: 16 RT rows of DP sums, then their maxima and weights.
-template <int DP, int RT>
-constexpr int slot_floats() { return 16 * RT * (DP + 2); }
+// Floats of one slot: the rows' DP sums, then their maxima and weights.
+template <int DP, int ROWS>
+constexpr int slot_floats() { return ROWS * (DP + 2); }
 
 // Target number of items: the workgroups that are resident at once.
-template <int DP, int RT>
-constexpr int item_target() { return kCus * (DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1); }
+constexpr int kItems = kCus * 2;
 
-// ---------------------------------------------------------------- main kernel
+// Positions of a tile that the waves share (what two workgroups' LDS holds).
+template <int DP>
+constexpr int wide_tile() { return DP == 256 ? 32 : 64; }
+
+// ---------------------------------------------------------------- pieces of both kernels
 // Transposed 16-bit read from LDS: within 16 lanes, lane 4 r + c reads 4
 // elements (row r, columns 4 c ..), and lane l receives column l of the four
 // rows.
@@ -151,16 +154,139 @@ __device__ __forceinline__ u32x2 lds_read_transposed(const uint16_t* p) {
 }
 
 template <int DT>
-__device__ __forceinline__ bool not_finite(uint32_t two) {
+__device__ __forceinline__ bool not_finite(u32x4 v) {
   const uint32_t e = DT == 0 ? 0x7c00u : 0x7f80u;
-  return (two & e) == e || ((two >> 16) & e) == e;
+  bool bad = false;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) bad |= (v[x] & e) == e || ((v[x] >> 16) & e) == e;
+  return bad;
 }
 
+// Offset (elements) of position pos of the sequence whose table row is given,
+// -1 if no page of the cache holds it.  pos is below max_pages * page_size.
+__device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int page, int pos) {
+  return in_range(page, a.num_pages) ? page * a.kv_page + (int64_t)(pos - pos / a.page_size * a.page_size) * a.kv_token
+                                     : (int64_t)-1;
+}
+
+// Queries of one row tile as matrix-core operand: lane col holds row
+// `row` (elements 32 s + 8 quad .. of it).  A negative scale turns their sign.
+template <int DP>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int node, int head, int quad,
+                                             u32x4 (&q)[DP / 32]) {
+  const uint16_t* p = a.q + (it.s.q0 + node) * a.q_token + head * a.q_head;
+  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+  for (int s = 0; s < DP / 32; ++s) {
+    q[s] = load8_16_masked(p, s * 32 + quad * 8, a.dim, true);
+    q[s] ^= u32x4{flip, flip, flip, flip};
+  }
+}
+
+// -inf into the scores of positions that row `node` does not see.  s[t][e] is
+// position key0 + 16 t + 4 quad + e; bit i of there: position key0 + i exists.
+__device__ __forceinline__ void mask_scores(const AttnArgs& a, const Item& it, int node, int key0, int quad,
+                                            uint32_t there, f32x4 (&s)[2]) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = t * 16 + quad * 4 + e;
+      const int j = key0 + i - it.s.ctx;
+      bool seen = (there >> i) & 1;
+      if (seen && j >= 0) {
+        if (a.mask) {
+          seen = j < a.mask_words * 64 && ((a.mask[(int64_t)(it.s.q0 + node) * a.ld_mask + j / 64] >> (j % 64)) & 1);
+        } else {
+          seen = j <= node;
+        }
+      }
+      if (!seen) s[t][e] = -INFINITY;
+    }
+}
+
+// One step of the running softmax of a row tile: raw scores in, weights out
+// (and as the 16-bit operand of the value product).  c = |scale| log2 e.  The
+// reference score m follows the maximum only when that has grown by 2^6 in
+// weight: until then the weights are at most 64, which loses nothing in fp32
+// sums and saves the scaling of l and o.
+template <int DT, int N>
+__device__ __forceinline__ u32x4 weigh(f32x4 (&s)[2], float c, float& m, float& l, f32x4 (&o)[N]) {
+  float top = fmaxf(fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[0].z, s[0].w)),
+                    fmaxf(fmaxf(s[1].x, s[1].y), fmaxf(s[1].z, s[1].w)));
+  top = max_over_lane_groups(top);
+  if (__any((top - m) * c > 6.f)) {
+    const float now = fmaxf(top, m);
+    const float shrink = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - now) * c);
+    l *= shrink;
+#pragma unroll
+    for (int d = 0; d < N; ++d) o[d] *= shrink;
+    m = now;
+  }
+  const float base = m == -INFINITY ? 0.f : -m * c;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e], c, base));
+      l += s[t][e];
+    }
+  return u32x4{cvt_pack2<DT>(s[0].x, s[0].y), cvt_pack2<DT>(s[0].z, s[0].w), cvt_pack2<DT>(s[1].x, s[1].y),
+               cvt_pack2<DT>(s[1].z, s[1].w)};
+}
+
+// Adds the value row p (position i of the step), which is not finite
+// throughout and was kept out of the products, to the rows that see it.
+template <int DT, int N>
+__device__ __forceinline__ void add_odd_value(const uint16_t* p, int i, int dim, int col, int quad, const f32x4 (&s)[2],
+                                              f32x4 (&o)[N]) {
+  const int src = (i % 16 / 4) * 16 + col;
+  float weight = 0.f;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = __shfl(s[t][e], src);
+      if (i / 16 == t && i % 4 == e) weight = x;
+    }
+#pragma unroll
+  for (int d = 0; d < N; ++d) {
+    const int c = d * 16 + quad * 4;
+    const u32x2 two = *reinterpret_cast<const u32x2*>(p + (c < dim ? c : dim - 4));
+    float x[4];
+    unpack2<DT>(two.x, &x[0], &x[1]);
+    unpack2<DT>(two.y, &x[2], &x[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (weight != 0.f) o[d][e] += weight * x[e];
+  }
+}
+
+__device__ __forceinline__ float log_sum(float base_log2, float sum) {
+  return sum > 0.f ? (base_log2 + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : sum == 0.f ? -INFINITY : sum;
+}
+
+// Scale of the exponent: never 0, which would turn a masked -inf into NaN.
+__device__ __forceinline__ float exponent_scale(const AttnArgs& a) { return fmaxf(fabsf(a.scale_log2), 1e-30f); }
+
+// Where a row's result goes: row maxima in units of log2.
+template <int DT>
+__device__ __forceinline__ void store_quad(const AttnArgs& a, int t, int h, int c, f32x4 x, float inv) {
+  if (c < a.dim)
+    *reinterpret_cast<u32x2*>(a.out + t * a.out_token + h * a.out_head + c) =
+        u32x2{cvt_pack2<DT>(x.x * inv, x.y * inv), cvt_pack2<DT>(x.z * inv, x.w * inv)};
+}
+
+// ---------------------------------------------------------------- few rows
+// Waves of a workgroup take different positions.  Keys go from memory straight
+// into the matrix core's operand; values pass through the wave's own part of
+// LDS, which turns rows into columns.  The next step's keys and values are on
+// their way while this one's are used.
 template <int DT, int DP, int RT>
-__global__ void __launch_bounds__(kWaves* kWave) attention_kernel(AttnArgs a, int slots, int max_slots) {
+__global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a, int slots, int max_slots) {
   constexpr int ROWS = 16 * RT;
   constexpr int KS = DP / 32;             // matrix-core steps of a score
-  constexpr int DT_ = DP / 16;            // tiles of the output's columns
+  constexpr int OT = DP / 16;             // tiles of the output's columns
   constexpr int PITCH = DP + 16;          // of a staged value row, in elements: rows start 8 banks apart
   constexpr int LPR = DP / 8;             // lanes per value row
   constexpr int RPL = kWave / LPR;        // value rows per load
@@ -171,68 +297,67 @@ __global__ void __launch_bounds__(kWaves* kWave) attention_kernel(AttnArgs a, in
   __shared__ float row_max[kWaves][ROWS], row_sum[kWaves][ROWS];
 
   Item it;
-  if (!find_item<ROWS>(a, blockIdx.x, slots, &it)) return;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  if (!find_item<ROWS, kTile>(a, blockIdx.x, slots, &it)) return;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, quad = lane >> 4;
   const int group = a.heads / a.kv_heads, rows = it.s.n * group;
   const int row0 = it.rt * ROWS;
   const int begin = it.split * it.tiles * kTile;
   const int end = min(it.s.len, begin + it.tiles * kTile);
+  const float c = exponent_scale(a);
 
-  // Queries: lane col of tile r holds row row0 + 16 r + col, elements
-  // 32 s + 8 quad .. of it.  Rows beyond the last read the last one.
   u32x4 q[RT][KS];
   int node[RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
+  for (int r = 0; r < RT; ++r) {  // rows beyond the last read the last one
     const int row = min(row0 + r * 16 + col, rows - 1);
     node[r] = row / group;
-    const uint16_t* p = a.q + (it.s.q0 + node[r]) * a.q_token + (it.h * group + row % group) * a.q_head;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) q[r][s] = load8_16_masked(p, s * 32 + quad * 8, a.dim, true);
+    load_queries<DP>(a, it, node[r], it.h * group + row % group, quad, q[r]);
   }
   const uint16_t* kbase = a.k + it.h * a.kv_head;
   const uint16_t* vbase = a.v + it.h * a.kv_head;
   const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
   uint16_t* stage = reinterpret_cast<uint16_t*>(lds + wave * STAGE);
 
-  f32x4 o[RT][DT_];
+  f32x4 o[RT][OT];
   float m[RT], l[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
-    for (int d = 0; d < DT_; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < OT; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int key0 = begin + wave * kKeys; key0 < end; key0 += kTile) {
-    // Lane l holds the cache row of position key0 + l % 32, or -1.
+  // Page of position key0 + lane % 32, or -1.
+  auto page_of = [&](int key0) {
     const int pos = key0 + (lane & 31);
-    int64_t at = -1;
-    if (pos < end) {
-      const int32_t page = table[pos / a.page_size];
-      if (in_range(page, a.num_pages)) at = page * a.kv_page + pos % a.page_size * a.kv_token;
-    }
-    const uint32_t there = (uint32_t)__ballot(at >= 0);  // both halves of the wave agree
-    const int64_t safe = at < 0 ? 0 : at;
-
-    u32x4 k[2][KS];
+    return pos < end ? table[pos / a.page_size] : -1;
+  };
+  u32x4 k[2][KS], v[VL];
+  auto load = [&](int64_t safe) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const uint16_t* p = kbase + __shfl(safe, t * 16 + col);
 #pragma unroll
       for (int s = 0; s < KS; ++s) k[t][s] = load8_16_masked(p, s * 32 + quad * 8, a.dim, true);
     }
-    u32x4 v[VL];
 #pragma unroll
     for (int i = 0; i < VL; ++i) {
-      const int r = i * RPL + lane / LPR;
-      const uint16_t* p = vbase + __shfl(safe, r);
+      const uint16_t* p = vbase + __shfl(safe, i * RPL + lane / LPR);
       const int d = lane % LPR * 8;
       v[i] = *reinterpret_cast<const u32x4*>(p + (d < a.dim ? d : a.dim - 8));
-      if (!((there >> r) & 1)) v[i] = u32x4{0u, 0u, 0u, 0u};
     }
+  };
+
+  int key0 = begin + wave * kKeys;
+  int page = page_of(key0);
+  int64_t at = cache_row(a, page, key0 + (lane & 31));
+  if (key0 < end) load(at < 0 ? 0 : at);
+  page = page_of(key0 + kTile);
+  for (; key0 < end; key0 += kTile) {
+    const uint32_t there = (uint32_t)__ballot(at >= 0);  // both halves of the wave agree
+    const int64_t here = at < 0 ? 0 : at;
 
     // Scores: lane holds positions key0 + 16 t + 4 quad + e of row col.
     f32x4 sc[RT][2];
@@ -243,89 +368,49 @@ __global__ void __launch_bounds__(kWaves* kWave) attention_kernel(AttnArgs a, in
         sc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < KS; ++s) sc[r][t] = mfma16x16x32<DT>(k[t][s], q[r][s], sc[r][t]);
-        sc[r][t] *= a.scale_log2;
       }
-    const bool drafted = key0 + kKeys > it.s.ctx;
-    if (drafted || there != 0xffffffffu) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = t * 16 + quad * 4 + e;
-            const int j = key0 + i - it.s.ctx;
-            bool seen = (there >> i) & 1;
-            if (seen && j >= 0) {
-              if (a.mask) {
-                seen = j < a.mask_words * 64 &&
-                       ((a.mask[(int64_t)(it.s.q0 + node[r]) * a.ld_mask + j / 64] >> (j % 64)) & 1);
-              } else {
-                seen = j <= node[r];
-              }
-            }
-            if (!seen) sc[r][t][e] = -INFINITY;
-          }
-    }
-
-    // Running maximum and sum; weights as the next operand.
-    u32x4 w[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float top = m[r];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[r][t][e]);
-      top = max_over_lane_groups(top);
-      const float base = top == -INFINITY ? 0.f : top;
-      if (__any(top != m[r])) {
-        const float shrink = __builtin_amdgcn_exp2f(m[r] - base);
-        l[r] *= shrink;
-#pragma unroll
-        for (int d = 0; d < DT_; ++d) o[r][d] *= shrink;
-      }
-      m[r] = top;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[r][t][e] = __builtin_amdgcn_exp2f(sc[r][t][e] - base);
-          l[r] += sc[r][t][e];
-        }
-        w[r][2 * t] = cvt_pack2<DT>(sc[r][t][0], sc[r][t][1]);
-        w[r][2 * t + 1] = cvt_pack2<DT>(sc[r][t][2], sc[r][t][3]);
-      }
-    }
 
     // Values that are not finite are kept out of the products with weight 0:
     // they are staged as 0 and added below to the rows that see them.
     uint32_t odd = 0;  // positions of the step with such values
-    if (drafted) {
+    const bool drafted = key0 + kKeys > it.s.ctx;
+    if (drafted || there != 0xffffffffu) {
 #pragma unroll
       for (int i = 0; i < VL; ++i) {
-        bool bad = false;
+        const int r = i * RPL + lane / LPR;
+        bool zero = !((there >> r) & 1);
+        const uint64_t lanes = __ballot(not_finite<DT>(v[i]) && !zero);
+        if (drafted && lanes) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) bad |= not_finite<DT>(v[i][x]);
-        const uint64_t lanes = __ballot(bad);
-        if (lanes) {
-#pragma unroll
-          for (int r = 0; r < RPL; ++r)
-            if ((lanes >> (r * LPR)) & ((LPR == 64 ? 0ull : 1ull << LPR) - 1ull)) odd |= 1u << (i * RPL + r);
-          if ((odd >> (i * RPL + lane / LPR)) & 1) v[i] = u32x4{0u, 0u, 0u, 0u};
+          for (int x = 0; x < RPL; ++x)
+            if ((lanes >> (x * LPR)) & ((1ull << LPR) - 1ull)) odd |= 1u << (i * RPL + x);
         }
+        if (zero || ((odd >> r) & 1)) v[i] = u32x4{0u, 0u, 0u, 0u};
       }
     }
-
-    // Values through LDS (the wave's own part): rows in, columns out.
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < VL; ++i)
       *reinterpret_cast<u32x4*>(stage + (i * RPL + lane / LPR) * PITCH + lane % LPR * 8) = v[i];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+
+    // The next step.
+    const int next = key0 + kTile;
+    at = cache_row(a, page, next + (lane & 31));
+    if (next < end) load(at < 0 ? 0 : at);
+    page = page_of(next + kTile);
+
+    if (drafted || there != 0xffffffffu) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) mask_scores(a, it, node[r], key0, quad, there, sc[r]);
+    }
+    u32x4 w[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) w[r] = weigh<DT, OT>(sc[r], c, m[r], l[r], o[r]);
+
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int d = 0; d < DT_; ++d) {
+    for (int d = 0; d < OT; ++d) {
       // Elements 0..3: positions 4 quad + 0..3 of the first 16, 4..7 of the second.
       const uint16_t* p = stage + (quad * 4 + (col >> 2)) * PITCH + d * 16 + (col & 3) * 4;
       const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * PITCH);
@@ -338,30 +423,9 @@ __global__ void __launch_bounds__(kWaves* kWave) attention_kernel(AttnArgs a, in
     while (odd) {
       const int i = __ffs(odd) - 1;
       odd &= odd - 1;
-      const uint16_t* p = vbase + __shfl(safe, i);
-      const int src = (i % 16 / 4) * 16 + col;
+      const uint16_t* p = vbase + __shfl(here, i);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float weight = 0.f;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = __shfl(sc[r][t][e], src);
-            if (i / 16 == t && i % 4 == e) weight = x;
-          }
-#pragma unroll
-        for (int d = 0; d < DT_; ++d) {
-          const int c = d * 16 + quad * 4;
-          const u32x2 two = *reinterpret_cast<const u32x2*>(p + (c < a.dim ? c : a.dim - 4));
-          float x[4];
-          unpack2<DT>(two.x, &x[0], &x[1]);
-          unpack2<DT>(two.y, &x[2], &x[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (weight != 0.f) o[r][d][e] += weight * x[e];
-        }
-      }
+      for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, sc[r], o[r]);
     }
   }
 
@@ -372,7 +436,7 @@ __global__ void __launch_bounds__(kWaves* kWave) attention_kernel(AttnArgs a, in
     x += __shfl_xor(x, 16);
     x += __shfl_xor(x, 32);
     if (quad == 0) {
-      row_max[wave][r * 16 + col] = m[r];
+      row_max[wave][r * 16 + col] = m[r] * c;
       row_sum[wave][r * 16 + col] = x;
     }
   }
@@ -381,17 +445,17 @@ __global__ void __launch_bounds__(kWaves* kWave) attention_kernel(AttnArgs a, in
   float* slot = nullptr;
   if (it.splits > 1) {
     if (it.slot >= max_slots) return;  // only where start is not ascending
-    slot = space(a).slots + (int64_t)it.slot * slot_floats<DP, RT>();
+    slot = space(a).slots + (int64_t)it.slot * slot_floats<DP, ROWS>();
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     __syncthreads();
 #pragma unroll
-    for (int d = 0; d < DT_; ++d)
+    for (int d = 0; d < OT; ++d)
       *reinterpret_cast<f32x4*>(join + (wave * 16 + col) * JP + d * 16 + quad * 4) = o[r][d];
     __syncthreads();
     for (int e = threadIdx.x; e < 16 * DP / 4; e += kWaves * kWave) {
-      const int i = e / (DP / 4), c = e % (DP / 4) * 4, in_tile = r * 16 + i, row = row0 + in_tile;
+      const int i = e / (DP / 4), cc = e % (DP / 4) * 4, in_tile = r * 16 + i, row = row0 + in_tile;
       if (row >= rows) continue;
       float top = row_max[0][in_tile];
 #pragma unroll
@@ -403,33 +467,218 @@ __global__ void __launch_bounds__(kWaves* kWave) attention_kernel(AttnArgs a, in
       for (int w = 0; w < kWaves; ++w) {
         const float f = __builtin_amdgcn_exp2f(row_max[w][in_tile] - base);
         sum += f * row_sum[w][in_tile];
-        x += *reinterpret_cast<const f32x4*>(join + (w * 16 + i) * JP + c) * f;
+        x += *reinterpret_cast<const f32x4*>(join + (w * 16 + i) * JP + cc) * f;
       }
       if (slot) {
-        *reinterpret_cast<f32x4*>(slot + in_tile * DP + c) = x;
-        if (c == 0) {
+        *reinterpret_cast<f32x4*>(slot + in_tile * DP + cc) = x;
+        if (cc == 0) {
           slot[ROWS * DP + in_tile] = top;
           slot[ROWS * DP + ROWS + in_tile] = sum;
         }
         continue;
       }
       const int t = it.s.q0 + row / group, h = it.h * group + row % group;
-      if (a.lse && c == 0)
-        a.lse[(int64_t)t * a.heads + h] = sum > 0.f ? (base + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : (sum == 0.f ? -INFINITY : sum);
-      if (c >= a.dim) continue;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      *reinterpret_cast<u32x2*>(a.out + t * a.out_token + h * a.out_head + c) =
-          u32x2{cvt_pack2<DT>(x.x * inv, x.y * inv), cvt_pack2<DT>(x.z * inv, x.w * inv)};
+      if (a.lse && cc == 0) a.lse[(int64_t)t * a.heads + h] = log_sum(base, sum);
+      store_quad<DT>(a, t, h, cc, x, sum == 0.f ? 0.f : 1.f / sum);
     }
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+// Waves of a workgroup take different rows (16 RT each) and share the tile of
+// positions in LDS, double-buffered; the tile after next is on its way in
+// registers while this one is used.  A tile costs one barrier.
+template <int DT, int DP, int RT>
+__global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnArgs a, int slots, int max_slots) {
+  constexpr int ROWS = kWaves * 16 * RT;
+  constexpr int KEYS = wide_tile<DP>();
+  constexpr int KS = DP / 32, OT = DP / 16;
+  constexpr int KP = DP + 8, VP = DP + 16;   // pitches: key rows 4 banks apart, value rows 8
+  constexpr int CPR = DP / 8;                // 16-byte pieces of a row
+  constexpr int RPP = kWaves * kWave / CPR;  // rows per pass
+  constexpr int PASS = KEYS / RPP;
+  __shared__ __align__(16) uint16_t kt[2][KEYS * KP];
+  __shared__ __align__(16) uint16_t vt[2][KEYS * VP];
+  __shared__ int64_t where[4][KEYS];         // cache rows of a tile's positions
+  __shared__ uint32_t odd_rows[2][KEYS / 32];
+
+  Item it;
+  if (!find_item<ROWS, KEYS>(a, blockIdx.x, slots, &it)) return;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int col = lane & 15, quad = lane >> 4;
+  const int group = a.heads / a.kv_heads, rows = it.s.n * group;
+  const int row0 = it.rt * ROWS + wave * 16 * RT;
+  const int begin = it.split * it.tiles * KEYS;
+  const int end = min(it.s.len, begin + it.tiles * KEYS);
+  const float c = exponent_scale(a);
+
+  u32x4 q[RT][KS];
+  int node[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = min(row0 + r * 16 + col, rows - 1);
+    node[r] = row / group;
+    load_queries<DP>(a, it, node[r], it.h * group + row % group, quad, q[r]);
+  }
+  const uint16_t* kbase = a.k + it.h * a.kv_head;
+  const uint16_t* vbase = a.v + it.h * a.kv_head;
+  const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
+
+  f32x4 o[RT][OT];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int d = 0; d < OT; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int piece = tid % CPR * 8, prow = tid / CPR;
+  const int clamped = piece < a.dim ? piece : a.dim - 8;
+  u32x4 kreg[PASS], vreg[PASS];
+  bool absent[PASS];
+  // Positions of tile n, by the first KEYS threads.
+  auto find_rows = [&](int n) {
+    const int pos = begin + n * KEYS + tid;
+    return tid < KEYS && pos < end ? cache_row(a, table[pos / a.page_size], pos) : (int64_t)-1;
+  };
+  auto fetch = [&](int n) {
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      const int64_t at = where[n & 3][prow + i * RPP];
+      absent[i] = at < 0;
+      kreg[i] = *reinterpret_cast<const u32x4*>(kbase + (at < 0 ? 0 : at) + clamped);
+      vreg[i] = *reinterpret_cast<const u32x4*>(vbase + (at < 0 ? 0 : at) + clamped);
+    }
+  };
+  // Tile n from the registers into its buffer.  A value row of a drafted node
+  // that is not finite is staged as 0 and noted.
+  auto stash = [&](int n) {
+    const bool drafted = begin + (n + 1) * KEYS > it.s.ctx;
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      const int r = prow + i * RPP;
+      u32x4 x = vreg[i];
+      if (absent[i]) x = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(&kt[n & 1][r * KP + piece]) = piece < a.dim ? kreg[i] : u32x4{0u, 0u, 0u, 0u};
+      if (drafted) {
+        const uint64_t lanes = __ballot(not_finite<DT>(x));
+        const int first = lane / CPR * CPR;
+        if (lanes && ((lanes >> first) & ((1ull << CPR) - 1ull))) {
+          x = u32x4{0u, 0u, 0u, 0u};
+          if (lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
+        }
+      }
+      *reinterpret_cast<u32x4*>(&vt[n & 1][r * VP + piece]) = x;
+    }
+  };
+
+  const int tiles = end > begin ? (end - begin + KEYS - 1) / KEYS : 0;
+  if (tid < KEYS) {
+#pragma unroll
+    for (int n = 0; n < 3; ++n) where[n][tid] = find_rows(n);
+  }
+  if (tid < 2 * (KEYS / 32)) odd_rows[tid / (KEYS / 32)][tid % (KEYS / 32)] = 0;
+  __syncthreads();
+  fetch(0);
+  stash(0);
+  fetch(1);
+  __syncthreads();
+
+  for (int n = 0; n < tiles; ++n) {
+    const int64_t later = find_rows(n + 3);
+    const uint16_t* kb = kt[n & 1];
+    const uint16_t* vb = vt[n & 1];
+#pragma unroll
+    for (int half = 0; half < KEYS / 32; ++half) {
+      const int key0 = begin + n * KEYS + half * 32;
+      const uint32_t there = (uint32_t)__ballot(where[n & 3][half * 32 + (lane & 31)] >= 0);
+      f32x4 sc[RT][2];
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) sc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const u32x4 kf = *reinterpret_cast<const u32x4*>(kb + (half * 32 + t * 16 + col) * KP + s * 32 + quad * 8);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) sc[r][t] = mfma16x16x32<DT>(kf, q[r][s], sc[r][t]);
+        }
+      if (key0 + 32 > it.s.ctx || there != 0xffffffffu) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) mask_scores(a, it, node[r], key0, quad, there, sc[r]);
+      }
+      u32x4 w[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) w[r] = weigh<DT, OT>(sc[r], c, m[r], l[r], o[r]);
+#pragma unroll
+      for (int d = 0; d < OT; ++d) {
+        const uint16_t* p = vb + (half * 32 + quad * 4 + (col >> 2)) * VP + d * 16 + (col & 3) * 4;
+        const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * VP);
+        const u32x4 vf = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf, w[r], o[r][d]);
+      }
+      uint32_t odd = odd_rows[n & 1][half];
+      while (odd) {
+        const int i = __ffs(odd) - 1;
+        odd &= odd - 1;
+        const uint16_t* p = vbase + where[n & 3][half * 32 + i];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, sc[r], o[r]);
+      }
+    }
+    // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
+    // between two barriers, and only where there can be any.
+    if (n + 1 < tiles) stash(n + 1);
+    if (tid < KEYS) where[(n + 3) & 3][tid] = later;
+    __syncthreads();
+    if (begin + (n + 1) * KEYS > it.s.ctx) {
+      if (tid < KEYS / 32) odd_rows[n & 1][tid] = 0;
+      __syncthreads();
+    }
+    if (n + 2 < tiles) fetch(n + 2);
+  }
+
+  float* slot = nullptr;
+  if (it.splits > 1) {
+    if (it.slot >= max_slots) return;  // only where start is not ascending
+    slot = space(a).slots + (int64_t)it.slot * slot_floats<DP, ROWS>();
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float sum = l[r];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    const int in_tile = (wave * RT + r) * 16 + col, row = row0 + r * 16 + col;
+    if (row >= rows) continue;
+    const float top = m[r] * c, base = m[r] == -INFINITY ? 0.f : top;
+    if (slot) {
+#pragma unroll
+      for (int d = 0; d < OT; ++d) *reinterpret_cast<f32x4*>(slot + in_tile * DP + d * 16 + quad * 4) = o[r][d];
+      if (quad == 0) {
+        slot[ROWS * DP + in_tile] = top;
+        slot[ROWS * DP + ROWS + in_tile] = sum;
+      }
+      continue;
+    }
+    const int t = it.s.q0 + row / group, h = it.h * group + row % group;
+    if (a.lse && quad == 0) a.lse[(int64_t)t * a.heads + h] = log_sum(base, sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int d = 0; d < OT; ++d) store_quad<DT>(a, t, h, d * 16 + quad * 4, o[r][d], inv);
   }
 }
 
 // ---------------------------------------------------------------- join of runs
 // One block per row (token, head): wave w takes runs w, w + 4, ...; 64 lanes
 // hold the DP columns.
-template <int DT, int DP, int RT>
+template <int DT, int DP, int ROWS, int KEYS>
 __global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a, int max_slots) {
-  constexpr int ROWS = 16 * RT, PER = DP / kWave;
+  constexpr int PER = DP / kWave;
   const Space sp = space(a);
   const int t = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -446,11 +695,11 @@ __global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a, int max
   if (first < 0) return;
   const Seq s = sequence(a, b);
   const int tiles = *sp.tiles;
-  const int splits = (key_tiles(s.len) + tiles - 1) / tiles, rts = row_tiles(s.n, group, ROWS);
+  const int splits = (key_tiles(s.len, KEYS) + tiles - 1) / tiles, rts = row_tiles(s.n, group, ROWS);
   const int row = (t - s.q0) * group + head % group, rt = row / ROWS, in_tile = row % ROWS;
   auto slot_of = [&](int split) {
     const int64_t i = min((int64_t)first + ((int64_t)split * a.kv_heads + head / group) * rts + rt, (int64_t)max_slots - 1);
-    return sp.slots + i * slot_floats<DP, RT>();
+    return sp.slots + i * slot_floats<DP, ROWS>();
   };
   float top = -INFINITY;
   for (int i = lane; i < splits; i += kWave) top = fmaxf(top, slot_of(i)[ROWS * DP + in_tile]);
@@ -483,52 +732,59 @@ __global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a, int max
         sum > 0.f ? (base + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : (sum == 0.f ? -INFINITY : sum);
 }
 
-template <int DT, int DP, int RT>
+// A launch takes WIDE kernels of 4 x 16 RT rows, or narrow ones of 16 RT.
+template <int DT, int DP, int RT, bool WIDE>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
-  constexpr int ROWS = 16 * RT, target = item_target<DP, RT>();
-  const int64_t group = a.heads / a.kv_heads;
+  constexpr int ROWS = (WIDE ? kWaves : 1) * 16 * RT;
+  constexpr int KEYS = WIDE ? wide_tile<DP>() : kTile;
+  const int64_t rows = (int64_t)a.T * (a.heads / a.kv_heads);
   // Every sequence has at most one row tile that is not full.
-  const int64_t tiles = a.T * group / ROWS + (a.B < a.T * group ? a.B : a.T * group);
-  attention_kernel<DT, DP, RT><<<(unsigned)(target + tiles * a.kv_heads), kWaves * kWave, 0, s>>>(a, target, 2 * target);
+  const int64_t tiles = rows / ROWS + (a.B < rows ? a.B : rows);
+  const unsigned grid = (unsigned)(kItems + tiles * a.kv_heads);
+  if constexpr (WIDE)
+    attention_rows_kernel<DT, DP, RT><<<grid, kWaves * kWave, 0, s>>>(a, kItems, 2 * kItems);
+  else
+    attention_kernel<DT, DP, RT><<<grid, kWaves * kWave, 0, s>>>(a, kItems, 2 * kItems);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  join_kernel<DT, DP, RT><<<(unsigned)(a.T * a.heads), kWaves * kWave, 0, s>>>(a, 2 * target);
+  join_kernel<DT, DP, ROWS, KEYS><<<(unsigned)(a.T * a.heads), kWaves * kWave, 0, s>>>(a, 2 * kItems);
   return hipGetLastError();
 }
 
-// Rows of a workgroup: what an average sequence has, up to what the registers
-// hold.
-int choose_rt(int64_t B, int64_t T, int group, int dp) {
+// Rows of a workgroup, from what an average sequence has: 16 or 32 in the
+// kernel whose waves split the positions, 64 or 128 in the one whose waves
+// split the rows.  256-wide heads leave registers for 16 and 64 only.
+int choose_rows(int64_t B, int64_t T, int group, int dp) {
   const int64_t rows = (T * group + B - 1) / B;
-  const int most = dp == 256 ? 2 : 4;
-  const int rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  return rt < most ? rt : most;
+  if (rows <= 16) return 16;
+  if (dp == 256) return 64;
+  return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
+template <int DT, int DP>
+hipError_t launch_rows(const AttnArgs& a, int rows, hipStream_t s) {
+  if (rows == 16) return launch<DT, DP, 1, false>(a, s);
+  if constexpr (DP != 256) {
+    if (rows == 32) return launch<DT, DP, 2, false>(a, s);
+    if (rows == 128) return launch<DT, DP, 2, true>(a, s);
+  }
+  return launch<DT, DP, 1, true>(a, s);
+}
+
 template <int DT>
 hipError_t launch_dt(const AttnArgs& a, hipStream_t s) {
-  const int dp = padded_dim(a.dim), rt = choose_rt(a.B, a.T, a.heads / a.kv_heads, dp);
-  switch (dp * 8 + rt) {
-    case 64 * 8 + 1: return launch<DT, 64, 1>(a, s);
-    case 64 * 8 + 2: return launch<DT, 64, 2>(a, s);
-    case 64 * 8 + 4: return launch<DT, 64, 4>(a, s);
-    case 128 * 8 + 1: return launch<DT, 128, 1>(a, s);
-    case 128 * 8 + 2: return launch<DT, 128, 2>(a, s);
-    case 128 * 8 + 4: return launch<DT, 128, 4>(a, s);
-    case 256 * 8 + 1: return launch<DT, 256, 1>(a, s);
-    default: return launch<DT, 256, 2>(a, s);
-  }
+  const int dp = padded_dim(a.dim), rows = choose_rows(a.B, a.T, a.heads / a.kv_heads, dp);
+  return dp == 64 ? launch_rows<DT, 64>(a, rows, s)
+                  : dp == 128 ? launch_rows<DT, 128>(a, rows, s) : launch_rows<DT, 256>(a, rows, s);
 }
 
 }  // namespace
 
 size_t attention_workspace(int32_t B, int32_t T, int32_t heads, int32_t kv_heads, int32_t dim) {
-  // 2 x item_target slots of 16 RT (DP + 2) floats, for every RT.
-  const int dp = padded_dim(dim), rt = choose_rt(B, T, heads / kv_heads, dp);
-  const int per_cu = dp * rt <= 128 ? 3 : dp * rt <= 256 ? 2 : 1;
-  return (4 + ((size_t)B + 3) / 4 * 4 + (size_t)2 * kCus * per_cu * 16 * rt * (dp + 2)) * 4;
+  const int dp = padded_dim(dim), rows = choose_rows(B, T, heads / kv_heads, dp);
+  return (4 + ((size_t)B + 3) / 4 * 4 + (size_t)2 * kItems * rows * (dp + 2)) * 4;
 }
 
 hipError_t launch_attention(const AttnArgs& args, int dtype, hipStream_t s) {
