@@ -3,11 +3,12 @@
 //   o[i, h] = sum_p w_p v[p] / sum_p w_p,  w_p = 2^(scale log2(e) q[i, h] . k[p] - m)
 //
 // Rows: the nodes of a sequence times the G = heads / kv_heads query heads that
-// share a key head, so one pass over the keys serves all of them.  A workgroup
-// takes 16 RT rows of one (sequence, key head) and a run of positions; its four
-// waves take 32 positions each in turn, with a running maximum and sum of their
-// own, and meet in LDS at the end.  Long sequences are cut into several runs
-// (so that few rows still fill the GPU); a second kernel joins those.
+// share a key head, so one pass over the keys serves all of them.  A line is one
+// row tile of one (sequence, key head), as long as the sequence's tiles of
+// positions.  The lines of a call, end to end, are cut into equal parts, one for
+// each workgroup that is resident at once: ragged lengths and few rows cost no
+// idle workgroups.  A line that lies in one part is finished there; the pieces
+// of one that was cut are joined by a second kernel.
 #include "decode_kernels.h"
 #include "lora_device.h"
 
@@ -21,7 +22,7 @@ constexpr int kCus = 256;
 
 __device__ __forceinline__ bool in_range(int32_t v, int32_t n) { return (uint32_t)v < (uint32_t)n; }
 
-// ---------------------------------------------------------------- work items
+// ---------------------------------------------------------------- work
 // A sequence as the kernels see it, whatever the buffers hold.
 struct Seq {
   int n, q0, ctx, len;  // nodes, first row, context, positions
@@ -38,110 +39,119 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
   return s;
 }
 
-struct Item {
-  Seq s;
-  int b, rt, h, split, splits, tiles;  // tiles: steps of a run
-  int slot;                            // of the partial result, if splits > 1
-};
+__device__ __forceinline__ int row_tiles(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
+__device__ __forceinline__ int key_tiles(int len, int keys) { return max((len + keys - 1) / keys, 1); }
 
-// Workspace: the run length and the first slot of each sequence (-1: not cut),
-// then the slots.  Every workgroup finds its item from the lengths by itself
-// (a wave's prefix sums over the sequences), so there is no plan to keep.
+// Number of parts: the workgroups that are resident at once.
+constexpr int kParts = kCus * 2;
+
+// Positions of a tile that the waves share (what two workgroups' LDS holds).
+template <int DP>
+constexpr int wide_tile() { return DP == 256 ? 32 : 64; }
+
+// Workspace: the tiles of a part and the first tile of each sequence's lines (a
+// line after the other: key heads, row tiles running fastest), then two slots
+// for each part: a line cut by the part's start leaves its sums in the first,
+// one cut by its end only in the second.
 struct Space {
-  int32_t* tiles;
+  int32_t* part;
   int32_t* first;
   float* slots;
 };
 
 __device__ __forceinline__ Space space(const AttnArgs& a) {
   Space w;
-  w.tiles = reinterpret_cast<int32_t*>(a.partial);
-  w.first = w.tiles + 4;
+  w.part = reinterpret_cast<int32_t*>(a.partial);
+  w.first = w.part + 4;
   w.slots = a.partial + 4 + (a.B + 3) / 4 * 4;
   return w;
-}
-
-__device__ __forceinline__ int row_tiles(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
-__device__ __forceinline__ int key_tiles(int len, int keys) { return max((len + keys - 1) / keys, 1); }
-
-// Item number `work`; false if there are fewer.  Items of a sequence: (run,
-// head) units in groups of eight, the row tiles of a group's units one after
-// the other, so that the row tiles that read the same keys are eight workgroups
-// apart and share an XCD's L2.
-template <int ROWS, int KEYS>
-__device__ __forceinline__ bool find_item(const AttnArgs& a, int work, int slots, Item* it) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int group = a.heads / a.kv_heads;
-  uint32_t units = 0;
-  for (int base = 0; base < a.B; base += kWave) {
-    int mine = 0;
-    if (base + lane < a.B) {
-      const Seq s = sequence(a, base + lane);
-      mine = row_tiles(s.n, group, ROWS) * key_tiles(s.len, KEYS) * a.kv_heads;
-    }
-    units += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(mine), kWave - 1);
-  }
-  const int tiles = max((int)((units + slots - 1) / slots), 1);
-  if (work == 0 && threadIdx.x == 0) *space(a).tiles = tiles;
-  int before = 0, slots_before = 0;
-  bool found = false;
-  for (int base = 0; base < a.B; base += kWave) {
-    Seq s{0, 0, 0, 0};
-    int rts = 0, splits = 0;
-    if (base + lane < a.B) {
-      s = sequence(a, base + lane);
-      rts = row_tiles(s.n, group, ROWS);
-      splits = (key_tiles(s.len, KEYS) + tiles - 1) / tiles;
-    }
-    const int count = rts * splits * a.kv_heads, cut = splits > 1 ? count : 0;
-    const int end = before + wave_inclusive_sum(count);
-    const int slot_end = slots_before + wave_inclusive_sum(cut);
-    if (work == 0 && threadIdx.x < kWave && base + lane < a.B)
-      space(a).first[base + lane] = splits > 1 ? slot_end - cut : -1;
-    const uint64_t m = __ballot(work < end && work >= end - count);
-    if (m && !found) {
-      found = true;
-      const int f = __ffsll((unsigned long long)m) - 1;
-      it->b = base + f;
-      it->s.n = __builtin_amdgcn_readlane(s.n, f);
-      it->s.q0 = __builtin_amdgcn_readlane(s.q0, f);
-      it->s.ctx = __builtin_amdgcn_readlane(s.ctx, f);
-      it->s.len = __builtin_amdgcn_readlane(s.len, f);
-      it->tiles = tiles;
-      it->splits = __builtin_amdgcn_readlane(splits, f);
-      const int rt_all = __builtin_amdgcn_readlane(rts, f);
-      const int u_all = it->splits * a.kv_heads, whole = u_all / 8 * 8;
-      int p = work - __builtin_amdgcn_readlane(end - count, f), u;
-      if (p < whole * rt_all) {
-        const int g = p / (8 * rt_all), r = p % (8 * rt_all);
-        it->rt = r / 8;
-        u = g * 8 + r % 8;
-      } else {
-        p -= whole * rt_all;
-        it->rt = p / (u_all - whole);
-        u = whole + p % (u_all - whole);
-      }
-      it->split = u / a.kv_heads;
-      it->h = u % a.kv_heads;
-      it->slot = __builtin_amdgcn_readlane(slot_end - cut, f) + u * rt_all + it->rt;
-    }
-    before = __builtin_amdgcn_readlane(end, kWave - 1);
-    slots_before = __builtin_amdgcn_readlane(slot_end, kWave - 1);
-    if (found && work != 0) break;
-  }
-  return found;
 }
 
 // Floats of one slot: the rows' DP sums, then their maxima and weights.
 template <int DP, int ROWS>
 constexpr int slot_floats() { return ROWS * (DP + 2); }
 
-// Target number of items: the workgroups that are resident at once.
-constexpr int kItems = kCus * 2;
+__device__ __forceinline__ int slot_of(int part, int part_tiles, int line) {
+  return 2 * part + (line <= part * part_tiles ? 0 : 1);
+}
 
-// Positions of a tile that the waves share (what two workgroups' LDS holds).
-template <int DP>
-constexpr int wide_tile() { return DP == 256 ? 32 : 64; }
+struct Place {
+  Seq s;
+  int b, h, rt, rts, tiles;  // sequence, key head, row tile of rts, tiles of the line
+  int line, at, end;         // first tile of the line, this piece's tiles (all from the call's start)
+  int part, part_tiles;
+};
+
+__device__ __forceinline__ void enter_sequence(const AttnArgs& a, int rows, int keys, int b, Place* p) {
+  p->b = b;
+  p->s = sequence(a, b);
+  p->s.n = __builtin_amdgcn_readfirstlane(p->s.n);
+  p->s.q0 = __builtin_amdgcn_readfirstlane(p->s.q0);
+  p->s.ctx = __builtin_amdgcn_readfirstlane(p->s.ctx);
+  p->s.len = __builtin_amdgcn_readfirstlane(p->s.len);
+  p->rts = row_tiles(p->s.n, a.heads / a.kv_heads, rows);
+  p->tiles = key_tiles(p->s.len, keys);
+}
+
+// The start of the workgroup's part; false if it has none.  Every wave finds
+// it by itself from the lengths (prefix sums over the sequences), so there is
+// no plan to keep.  Neighbouring parts, whose lines often read the same keys,
+// go to one XCD and its L2.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int group = a.heads / a.kv_heads;
+  const int part = (blockIdx.x & 7) * (kParts / 8) + (blockIdx.x >> 3);
+  auto tiles_of = [&](int b) {
+    if (b >= a.B) return 0;
+    const Seq s = sequence(a, b);
+    return row_tiles(s.n, group, ROWS) * a.kv_heads * key_tiles(s.len, KEYS);
+  };
+  uint32_t total = 0;
+  for (int base = 0; base < a.B; base += kWave)
+    total += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(tiles_of(base + lane)), kWave - 1);
+  const int part_tiles = max((int)((total + kParts - 1) / kParts), 1);
+  p->part = part;
+  p->part_tiles = part_tiles;
+  p->at = part * part_tiles;
+  p->end = min((int)total, p->at + part_tiles);
+  if (part == 0 && threadIdx.x == 0) *space(a).part = part_tiles;
+  int before = 0, b = -1, start = 0;
+  for (int base = 0; base < a.B; base += kWave) {
+    const int mine = tiles_of(base + lane);
+    const int end = before + wave_inclusive_sum(mine);
+    if (part == 0 && threadIdx.x < kWave && base + lane < a.B) space(a).first[base + lane] = end - mine;
+    const uint64_t m = __ballot(p->at < end && p->at >= end - mine);
+    if (m && b < 0) {
+      const int f = __ffsll((unsigned long long)m) - 1;
+      b = base + f;
+      start = __builtin_amdgcn_readlane(end - mine, f);
+    }
+    before = __builtin_amdgcn_readlane(end, kWave - 1);
+    if (b >= 0 && part != 0) break;
+  }
+  if (b < 0 || p->at >= p->end) return false;
+  enter_sequence(a, ROWS, KEYS, b, p);
+  const int line = (p->at - start) / p->tiles;
+  p->h = line / p->rts;
+  p->rt = line % p->rts;
+  p->line = start + line * p->tiles;
+  return true;
+}
+
+// The line after the one of *p, in a part that goes on.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ void next_line(const AttnArgs& a, Place* p) {
+  p->line += p->tiles;
+  p->at = p->line;
+  if (++p->rt < p->rts) return;
+  p->rt = 0;
+  if (++p->h < a.kv_heads) return;
+  p->h = 0;
+  int b = p->b + 1;
+  do enter_sequence(a, ROWS, KEYS, b, p);
+  while (p->rts == 0 && ++b < a.B);
+}
 
 // ---------------------------------------------------------------- pieces of both kernels
 // Transposed 16-bit read from LDS: within 16 lanes, lane 4 r + c reads 4
@@ -172,7 +182,7 @@ __device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int page, int po
 // Queries of one row tile as matrix-core operand: lane col holds row
 // `row` (elements 32 s + 8 quad .. of it).  A negative scale turns their sign.
 template <int DP>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, int node, int head, int quad,
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Place& it, int node, int head, int quad,
                                              u32x4 (&q)[DP / 32]) {
   const uint16_t* p = a.q + (it.s.q0 + node) * a.q_token + head * a.q_head;
   const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -183,26 +193,39 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
   }
 }
 
-// -inf into the scores of positions that row `node` does not see.  s[t][e] is
-// position key0 + 16 t + 4 quad + e; bit i of there: position key0 + i exists.
-__device__ __forceinline__ void mask_scores(const AttnArgs& a, const Item& it, int node, int key0, int quad,
-                                            uint32_t there, f32x4 (&s)[2]) {
+// Which of the positions key0 .. key0 + 31 row `node` sees, one bit each;
+// `there`: the positions that exist.
+__device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const Place& it, int node, int key0, uint32_t there) {
+  const int j0 = key0 - it.s.ctx;  // the node at position key0; at least -31 where it matters
+  if (j0 <= -32) return there;
+  uint32_t bits;
+  if (a.mask) {
+    // 32 bits from bit j0 on of the row's words; all ones before bit 0, zeros
+    // behind the last word.
+    const uint64_t* row = a.mask + (int64_t)(it.s.q0 + node) * a.ld_mask;
+    const int w = j0 >> 6, sh = j0 & 63, last = a.mask_words - 1;
+    uint64_t lo = w < 0 ? ~0ull : 0ull, hi = 0ull;
+    if (last >= 0) {
+      const uint64_t x = row[min(max(w, 0), last)], y = row[min(w + 1, last)];
+      if (w >= 0 && w <= last) lo = x;
+      if (w < last) hi = y;
+    }
+    bits = (uint32_t)((lo >> sh) | (sh ? hi << (64 - sh) : 0ull));
+  } else {
+    const int ones = node - j0 + 1;
+    bits = ones >= 32 ? ~0u : ones <= 0 ? 0u : (1u << ones) - 1u;
+  }
+  return bits & there;
+}
+
+// -inf into the scores of positions that are not seen: s[t][e] is position
+// 16 t + 4 quad + e of the 32.
+__device__ __forceinline__ void mask_scores(uint32_t seen, int quad, f32x4 (&s)[2]) {
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = t * 16 + quad * 4 + e;
-      const int j = key0 + i - it.s.ctx;
-      bool seen = (there >> i) & 1;
-      if (seen && j >= 0) {
-        if (a.mask) {
-          seen = j < a.mask_words * 64 && ((a.mask[(int64_t)(it.s.q0 + node) * a.ld_mask + j / 64] >> (j % 64)) & 1);
-        } else {
-          seen = j <= node;
-        }
-      }
-      if (!seen) s[t][e] = -INFINITY;
-    }
+    for (int e = 0; e < 4; ++e)
+      if (!((seen >> (t * 16 + quad * 4 + e)) & 1)) s[t][e] = -INFINITY;
 }
 
 // One step of the running softmax of a row tile: raw scores in, weights out
@@ -282,198 +305,172 @@ __device__ __forceinline__ void store_quad(const AttnArgs& a, int t, int h, int 
 // into the matrix core's operand; values pass through the wave's own part of
 // LDS, which turns rows into columns.  The next step's keys and values are on
 // their way while this one's are used.
-template <int DT, int DP, int RT>
-__global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a, int slots, int max_slots) {
-  constexpr int ROWS = 16 * RT;
+template <int DT, int DP>
+__global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a) {
+  constexpr int ROWS = 16;
   constexpr int KS = DP / 32;             // matrix-core steps of a score
   constexpr int OT = DP / 16;             // tiles of the output's columns
   constexpr int PITCH = DP + 16;          // of a staged value row, in elements: rows start 8 banks apart
   constexpr int LPR = DP / 8;             // lanes per value row
   constexpr int RPL = kWave / LPR;        // value rows per load
   constexpr int VL = kKeys / RPL;         // loads per step
-  constexpr int STAGE = kKeys * PITCH * 2;                    // bytes of one wave's values
-  constexpr int JOIN = 16 * (DP + 4) * 4;                     // bytes of one wave's sums of 16 rows
+  constexpr int JP = DP + 4;              // pitch of a row of sums
+  constexpr int STAGE = kKeys * PITCH * 2;  // bytes of one wave's values
+  constexpr int JOIN = ROWS * JP * 4;       // bytes of one wave's sums
   __shared__ __align__(16) uint8_t lds[kWaves * (STAGE > JOIN ? STAGE : JOIN)];
   __shared__ float row_max[kWaves][ROWS], row_sum[kWaves][ROWS];
 
-  Item it;
-  if (!find_item<ROWS, kTile>(a, blockIdx.x, slots, &it)) return;
+  Place it;
+  if (!find_part<ROWS, kTile>(a, &it)) return;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, quad = lane >> 4;
-  const int group = a.heads / a.kv_heads, rows = it.s.n * group;
-  const int row0 = it.rt * ROWS;
-  const int begin = it.split * it.tiles * kTile;
-  const int end = min(it.s.len, begin + it.tiles * kTile);
+  const int group = a.heads / a.kv_heads;
   const float c = exponent_scale(a);
-
-  u32x4 q[RT][KS];
-  int node[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {  // rows beyond the last read the last one
-    const int row = min(row0 + r * 16 + col, rows - 1);
-    node[r] = row / group;
-    load_queries<DP>(a, it, node[r], it.h * group + row % group, quad, q[r]);
-  }
-  const uint16_t* kbase = a.k + it.h * a.kv_head;
-  const uint16_t* vbase = a.v + it.h * a.kv_head;
-  const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
   uint16_t* stage = reinterpret_cast<uint16_t*>(lds + wave * STAGE);
+  float* join = reinterpret_cast<float*>(lds);
 
-  f32x4 o[RT][OT];
-  float m[RT], l[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-#pragma unroll
-    for (int d = 0; d < OT; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (;;) {
+    const int rows = it.s.n * group, row0 = it.rt * ROWS;
+    const int from = it.at - it.line, to = min(it.tiles, it.end - it.line);
+    const int begin = from * kTile, end = min(it.s.len, to * kTile);
 
-  // Page of position key0 + lane % 32, or -1.
-  auto page_of = [&](int key0) {
-    const int pos = key0 + (lane & 31);
-    return pos < end ? table[pos / a.page_size] : -1;
-  };
-  u32x4 k[2][KS], v[VL];
-  auto load = [&](int64_t safe) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint16_t* p = kbase + __shfl(safe, t * 16 + col);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) k[t][s] = load8_16_masked(p, s * 32 + quad * 8, a.dim, true);
-    }
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const uint16_t* p = vbase + __shfl(safe, i * RPL + lane / LPR);
-      const int d = lane % LPR * 8;
-      v[i] = *reinterpret_cast<const u32x4*>(p + (d < a.dim ? d : a.dim - 8));
-    }
-  };
+    const int my_row = min(row0 + col, rows - 1);  // rows beyond the last read the last one
+    const int node = my_row / group;
+    u32x4 q[KS];
+    load_queries<DP>(a, it, node, it.h * group + my_row % group, quad, q);
+    const uint16_t* kbase = a.k + it.h * a.kv_head;
+    const uint16_t* vbase = a.v + it.h * a.kv_head;
+    const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
 
-  int key0 = begin + wave * kKeys;
-  int page = page_of(key0);
-  int64_t at = cache_row(a, page, key0 + (lane & 31));
-  if (key0 < end) load(at < 0 ? 0 : at);
-  page = page_of(key0 + kTile);
-  for (; key0 < end; key0 += kTile) {
-    const uint32_t there = (uint32_t)__ballot(at >= 0);  // both halves of the wave agree
-    const int64_t here = at < 0 ? 0 : at;
-
-    // Scores: lane holds positions key0 + 16 t + 4 quad + e of row col.
-    f32x4 sc[RT][2];
+    f32x4 o[OT];
+    float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int d = 0; d < OT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // Page of position key0 + lane % 32, or -1.
+    auto page_of = [&](int key0) {
+      const int pos = key0 + (lane & 31);
+      return pos < end ? table[pos / a.page_size] : -1;
+    };
+    u32x4 k[2][KS], v[VL];
+    auto load = [&](int64_t safe) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        sc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const uint16_t* p = kbase + __shfl(safe, t * 16 + col);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) sc[r][t] = mfma16x16x32<DT>(k[t][s], q[r][s], sc[r][t]);
+        for (int s = 0; s < KS; ++s) k[t][s] = load8_16_masked(p, s * 32 + quad * 8, a.dim, true);
       }
-
-    // Values that are not finite are kept out of the products with weight 0:
-    // they are staged as 0 and added below to the rows that see them.
-    uint32_t odd = 0;  // positions of the step with such values
-    const bool drafted = key0 + kKeys > it.s.ctx;
-    if (drafted || there != 0xffffffffu) {
 #pragma unroll
       for (int i = 0; i < VL; ++i) {
-        const int r = i * RPL + lane / LPR;
-        bool zero = !((there >> r) & 1);
-        const uint64_t lanes = __ballot(not_finite<DT>(v[i]) && !zero);
-        if (drafted && lanes) {
+        const uint16_t* p = vbase + __shfl(safe, i * RPL + lane / LPR);
+        const int d = lane % LPR * 8;
+        v[i] = *reinterpret_cast<const u32x4*>(p + (d < a.dim ? d : a.dim - 8));
+      }
+    };
+
+    int key0 = begin + wave * kKeys;
+    int page = page_of(key0);
+    int64_t at = cache_row(a, page, key0 + (lane & 31));
+    if (key0 < end) load(at < 0 ? 0 : at);
+    page = page_of(key0 + kTile);
+    for (; key0 < end; key0 += kTile) {
+      const uint32_t there = (uint32_t)__ballot(at >= 0);  // both halves of the wave agree
+      const int64_t here = at < 0 ? 0 : at;
+
+      // Scores: lane holds positions key0 + 16 t + 4 quad + e of row col.
+      f32x4 sc[2];
 #pragma unroll
-          for (int x = 0; x < RPL; ++x)
-            if ((lanes >> (x * LPR)) & ((1ull << LPR) - 1ull)) odd |= 1u << (i * RPL + x);
+      for (int t = 0; t < 2; ++t) {
+        sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) sc[t] = mfma16x16x32<DT>(k[t][s], q[s], sc[t]);
+      }
+
+      // Values that are not finite are kept out of the products with weight 0:
+      // they are staged as 0 and added below to the rows that see them.
+      uint32_t odd = 0;  // positions of the step with such values
+      const bool drafted = key0 + kKeys > it.s.ctx;
+      if (drafted || there != 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < VL; ++i) {
+          const int r = i * RPL + lane / LPR;
+          const bool zero = !((there >> r) & 1);
+          const uint64_t lanes = __ballot(not_finite<DT>(v[i]) && !zero);
+          if (drafted && lanes) {
+#pragma unroll
+            for (int x = 0; x < RPL; ++x)
+              if ((lanes >> (x * LPR)) & ((1ull << LPR) - 1ull)) odd |= 1u << (i * RPL + x);
+          }
+          if (zero || ((odd >> r) & 1)) v[i] = u32x4{0u, 0u, 0u, 0u};
         }
-        if (zero || ((odd >> r) & 1)) v[i] = u32x4{0u, 0u, 0u, 0u};
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int i = 0; i < VL; ++i)
+        *reinterpret_cast<u32x4*>(stage + (i * RPL + lane / LPR) * PITCH + lane % LPR * 8) = v[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+
+      // The next step.
+      const int next = key0 + kTile;
+      at = cache_row(a, page, next + (lane & 31));
+      if (next < end) load(at < 0 ? 0 : at);
+      page = page_of(next + kTile);
+
+      if (drafted || there != 0xffffffffu) mask_scores(seen_bits(a, it, node, key0, there), quad, sc);
+      const u32x4 w = weigh<DT, OT>(sc, c, m, l, o);
+
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int d = 0; d < OT; ++d) {
+        // Elements 0..3: positions 4 quad + 0..3 of the first 16, 4..7 of the second.
+        const uint16_t* p = stage + (quad * 4 + (col >> 2)) * PITCH + d * 16 + (col & 3) * 4;
+        const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * PITCH);
+        o[d] = mfma16x16x32<DT>(u32x4{lo.x, lo.y, hi.x, hi.y}, w, o[d]);
+      }
+      __builtin_amdgcn_wave_barrier();
+
+      while (odd) {
+        const int i = __ffs(odd) - 1;
+        odd &= odd - 1;
+        add_odd_value<DT, OT>(vbase + __shfl(here, i), i, a.dim, col, quad, sc, o);
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-    for (int i = 0; i < VL; ++i)
-      *reinterpret_cast<u32x4*>(stage + (i * RPL + lane / LPR) * PITCH + lane % LPR * 8) = v[i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
-    // The next step.
-    const int next = key0 + kTile;
-    at = cache_row(a, page, next + (lane & 31));
-    if (next < end) load(at < 0 ? 0 : at);
-    page = page_of(next + kTile);
-
-    if (drafted || there != 0xffffffffu) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) mask_scores(a, it, node[r], key0, quad, there, sc[r]);
-    }
-    u32x4 w[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) w[r] = weigh<DT, OT>(sc[r], c, m[r], l[r], o[r]);
-
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int d = 0; d < OT; ++d) {
-      // Elements 0..3: positions 4 quad + 0..3 of the first 16, 4..7 of the second.
-      const uint16_t* p = stage + (quad * 4 + (col >> 2)) * PITCH + d * 16 + (col & 3) * 4;
-      const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * PITCH);
-      const u32x4 vt = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-      for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vt, w[r], o[r][d]);
-    }
-    __builtin_amdgcn_wave_barrier();
-
-    while (odd) {
-      const int i = __ffs(odd) - 1;
-      odd &= odd - 1;
-      const uint16_t* p = vbase + __shfl(here, i);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, sc[r], o[r]);
-    }
-  }
-
-  // Join the waves: 16 rows at a time through LDS.
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    float x = l[r];
-    x += __shfl_xor(x, 16);
-    x += __shfl_xor(x, 32);
+    // Join the waves.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
     if (quad == 0) {
-      row_max[wave][r * 16 + col] = m[r] * c;
-      row_sum[wave][r * 16 + col] = x;
+      row_max[wave][col] = m * c;
+      row_sum[wave][col] = l;
     }
-  }
-  constexpr int JP = DP + 4;
-  float* join = reinterpret_cast<float*>(lds);
-  float* slot = nullptr;
-  if (it.splits > 1) {
-    if (it.slot >= max_slots) return;  // only where start is not ascending
-    slot = space(a).slots + (int64_t)it.slot * slot_floats<DP, ROWS>();
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    __syncthreads();
+    __syncthreads();  // every wave is done with its values
 #pragma unroll
     for (int d = 0; d < OT; ++d)
-      *reinterpret_cast<f32x4*>(join + (wave * 16 + col) * JP + d * 16 + quad * 4) = o[r][d];
+      *reinterpret_cast<f32x4*>(join + (wave * ROWS + col) * JP + d * 16 + quad * 4) = o[d];
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * DP / 4; e += kWaves * kWave) {
-      const int i = e / (DP / 4), cc = e % (DP / 4) * 4, in_tile = r * 16 + i, row = row0 + in_tile;
+    float* slot = nullptr;
+    if (to - from < it.tiles)
+      slot = space(a).slots + (int64_t)slot_of(it.part, it.part_tiles, it.line) * slot_floats<DP, ROWS>();
+    for (int e = threadIdx.x; e < ROWS * DP / 4; e += kWaves * kWave) {
+      const int i = e / (DP / 4), cc = e % (DP / 4) * 4, row = row0 + i;
       if (row >= rows) continue;
-      float top = row_max[0][in_tile];
+      float top = row_max[0][i];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, row_max[w][in_tile]);
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, row_max[w][i]);
       const float base = top == -INFINITY ? 0.f : top;
       float sum = 0.f;
       f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(row_max[w][in_tile] - base);
-        sum += f * row_sum[w][in_tile];
-        x += *reinterpret_cast<const f32x4*>(join + (w * 16 + i) * JP + cc) * f;
+        const float f = __builtin_amdgcn_exp2f(row_max[w][i] - base);
+        sum += f * row_sum[w][i];
+        x += *reinterpret_cast<const f32x4*>(join + (w * ROWS + i) * JP + cc) * f;
       }
       if (slot) {
-        *reinterpret_cast<f32x4*>(slot + in_tile * DP + cc) = x;
+        *reinterpret_cast<f32x4*>(slot + i * DP + cc) = x;
         if (cc == 0) {
-          slot[ROWS * DP + in_tile] = top;
-          slot[ROWS * DP + ROWS + in_tile] = sum;
+          slot[ROWS * DP + i] = top;
+          slot[ROWS * DP + ROWS + i] = sum;
         }
         continue;
       }
@@ -481,6 +478,9 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
       if (a.lse && cc == 0) a.lse[(int64_t)t * a.heads + h] = log_sum(base, sum);
       store_quad<DT>(a, t, h, cc, x, sum == 0.f ? 0.f : 1.f / sum);
     }
+    if (it.line + it.tiles >= it.end) return;
+    __syncthreads();
+    next_line<ROWS, kTile>(a, &it);
   }
 }
 
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
 // positions in LDS, double-buffered; the tile after next is on its way in
 // registers while this one is used.  A tile costs one barrier.
 template <int DT, int DP, int RT>
-__global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnArgs a, int slots, int max_slots) {
+__global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnArgs a) {
   constexpr int ROWS = kWaves * 16 * RT;
   constexpr int KEYS = wide_tile<DP>();
   constexpr int KS = DP / 32, OT = DP / 16;
@@ -502,186 +502,201 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
   __shared__ int64_t where[4][KEYS];         // cache rows of a tile's positions
   __shared__ uint32_t odd_rows[2][KEYS / 32];
 
-  Item it;
-  if (!find_item<ROWS, KEYS>(a, blockIdx.x, slots, &it)) return;
+  Place it;
+  if (!find_part<ROWS, KEYS>(a, &it)) return;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int col = lane & 15, quad = lane >> 4;
-  const int group = a.heads / a.kv_heads, rows = it.s.n * group;
-  const int row0 = it.rt * ROWS + wave * 16 * RT;
-  const int begin = it.split * it.tiles * KEYS;
-  const int end = min(it.s.len, begin + it.tiles * KEYS);
+  const int group = a.heads / a.kv_heads;
   const float c = exponent_scale(a);
-
-  u32x4 q[RT][KS];
-  int node[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = min(row0 + r * 16 + col, rows - 1);
-    node[r] = row / group;
-    load_queries<DP>(a, it, node[r], it.h * group + row % group, quad, q[r]);
-  }
-  const uint16_t* kbase = a.k + it.h * a.kv_head;
-  const uint16_t* vbase = a.v + it.h * a.kv_head;
-  const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
-
-  f32x4 o[RT][OT];
-  float m[RT], l[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-#pragma unroll
-    for (int d = 0; d < OT; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
   const int piece = tid % CPR * 8, prow = tid / CPR;
   const int clamped = piece < a.dim ? piece : a.dim - 8;
-  u32x4 kreg[PASS], vreg[PASS];
-  bool absent[PASS];
-  // Positions of tile n, by the first KEYS threads.
-  auto find_rows = [&](int n) {
-    const int pos = begin + n * KEYS + tid;
-    return tid < KEYS && pos < end ? cache_row(a, table[pos / a.page_size], pos) : (int64_t)-1;
-  };
-  auto fetch = [&](int n) {
-#pragma unroll
-    for (int i = 0; i < PASS; ++i) {
-      const int64_t at = where[n & 3][prow + i * RPP];
-      absent[i] = at < 0;
-      kreg[i] = *reinterpret_cast<const u32x4*>(kbase + (at < 0 ? 0 : at) + clamped);
-      vreg[i] = *reinterpret_cast<const u32x4*>(vbase + (at < 0 ? 0 : at) + clamped);
-    }
-  };
-  // Tile n from the registers into its buffer.  A value row of a drafted node
-  // that is not finite is staged as 0 and noted.
-  auto stash = [&](int n) {
-    const bool drafted = begin + (n + 1) * KEYS > it.s.ctx;
-#pragma unroll
-    for (int i = 0; i < PASS; ++i) {
-      const int r = prow + i * RPP;
-      u32x4 x = vreg[i];
-      if (absent[i]) x = u32x4{0u, 0u, 0u, 0u};
-      *reinterpret_cast<u32x4*>(&kt[n & 1][r * KP + piece]) = piece < a.dim ? kreg[i] : u32x4{0u, 0u, 0u, 0u};
-      if (drafted) {
-        const uint64_t lanes = __ballot(not_finite<DT>(x));
-        const int first = lane / CPR * CPR;
-        if (lanes && ((lanes >> first) & ((1ull << CPR) - 1ull))) {
-          x = u32x4{0u, 0u, 0u, 0u};
-          if (lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
-        }
-      }
-      *reinterpret_cast<u32x4*>(&vt[n & 1][r * VP + piece]) = x;
-    }
-  };
 
-  const int tiles = end > begin ? (end - begin + KEYS - 1) / KEYS : 0;
-  if (tid < KEYS) {
-#pragma unroll
-    for (int n = 0; n < 3; ++n) where[n][tid] = find_rows(n);
-  }
-  if (tid < 2 * (KEYS / 32)) odd_rows[tid / (KEYS / 32)][tid % (KEYS / 32)] = 0;
-  __syncthreads();
-  fetch(0);
-  stash(0);
-  fetch(1);
-  __syncthreads();
+  for (;;) {
+    const int rows = it.s.n * group, row0 = it.rt * ROWS + wave * 16 * RT;
+    const int from = it.at - it.line, to = min(it.tiles, it.end - it.line);
+    const int begin = from * KEYS, end = min(it.s.len, to * KEYS);
 
-  for (int n = 0; n < tiles; ++n) {
-    const int64_t later = find_rows(n + 3);
-    const uint16_t* kb = kt[n & 1];
-    const uint16_t* vb = vt[n & 1];
+    u32x4 q[RT][KS];
+    int node[RT];
 #pragma unroll
-    for (int half = 0; half < KEYS / 32; ++half) {
-      const int key0 = begin + n * KEYS + half * 32;
-      const uint32_t there = (uint32_t)__ballot(where[n & 3][half * 32 + (lane & 31)] >= 0);
-      f32x4 sc[RT][2];
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) sc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const u32x4 kf = *reinterpret_cast<const u32x4*>(kb + (half * 32 + t * 16 + col) * KP + s * 32 + quad * 8);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) sc[r][t] = mfma16x16x32<DT>(kf, q[r][s], sc[r][t]);
-        }
-      if (key0 + 32 > it.s.ctx || there != 0xffffffffu) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) mask_scores(a, it, node[r], key0, quad, there, sc[r]);
-      }
-      u32x4 w[RT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) w[r] = weigh<DT, OT>(sc[r], c, m[r], l[r], o[r]);
-#pragma unroll
-      for (int d = 0; d < OT; ++d) {
-        const uint16_t* p = vb + (half * 32 + quad * 4 + (col >> 2)) * VP + d * 16 + (col & 3) * 4;
-        const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * VP);
-        const u32x4 vf = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-        for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf, w[r], o[r][d]);
-      }
-      uint32_t odd = odd_rows[n & 1][half];
-      while (odd) {
-        const int i = __ffs(odd) - 1;
-        odd &= odd - 1;
-        const uint16_t* p = vbase + where[n & 3][half * 32 + i];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, sc[r], o[r]);
-      }
+    for (int r = 0; r < RT; ++r) {
+      const int row = min(row0 + r * 16 + col, rows - 1);
+      node[r] = row / group;
+      load_queries<DP>(a, it, node[r], it.h * group + row % group, quad, q[r]);
     }
-    // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
-    // between two barriers, and only where there can be any.
-    if (n + 1 < tiles) stash(n + 1);
-    if (tid < KEYS) where[(n + 3) & 3][tid] = later;
+    const uint16_t* kbase = a.k + it.h * a.kv_head;
+    const uint16_t* vbase = a.v + it.h * a.kv_head;
+    const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
+
+    f32x4 o[RT][OT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int d = 0; d < OT; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    u32x4 kreg[PASS], vreg[PASS];
+    bool absent[PASS];
+    // Page of a position of tile n (the one this thread looks up), and the cache
+    // row that follows from it.  The two are apart so that the page is on its
+    // way during a whole tile.
+    auto find_page = [&](int n) { return table[min(begin + n * KEYS + tid % KEYS, max(end - 1, 0)) / a.page_size]; };
+    auto find_row = [&](int n, int page) {
+      const int pos = begin + n * KEYS + tid % KEYS;
+      return pos < end ? cache_row(a, page, pos) : (int64_t)-1;
+    };
+    auto fetch = [&](int n) {
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) {
+        const int64_t at = where[n & 3][prow + i * RPP];
+        absent[i] = at < 0;
+        kreg[i] = *reinterpret_cast<const u32x4*>(kbase + (at < 0 ? 0 : at) + clamped);
+        vreg[i] = *reinterpret_cast<const u32x4*>(vbase + (at < 0 ? 0 : at) + clamped);
+      }
+    };
+    // Tile n from the registers into its buffer.  A value row of a drafted node
+    // that is not finite is staged as 0 and noted.
+    auto stash = [&](int n) {
+      const bool drafted = begin + (n + 1) * KEYS > it.s.ctx;
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) {
+        const int r = prow + i * RPP;
+        u32x4 x = vreg[i];
+        if (absent[i]) x = u32x4{0u, 0u, 0u, 0u};
+        *reinterpret_cast<u32x4*>(&kt[n & 1][r * KP + piece]) = piece < a.dim ? kreg[i] : u32x4{0u, 0u, 0u, 0u};
+        if (drafted) {
+          const uint64_t lanes = __ballot(not_finite<DT>(x));
+          const int first = lane / CPR * CPR;
+          if (lanes && ((lanes >> first) & ((1ull << CPR) - 1ull))) {
+            x = u32x4{0u, 0u, 0u, 0u};
+            if (lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
+          }
+        }
+        *reinterpret_cast<u32x4*>(&vt[n & 1][r * VP + piece]) = x;
+      }
+    };
+
+    const int tiles = end > begin ? (end - begin + KEYS - 1) / KEYS : 0;
+    if (a.max_pages > 0) {
+      int page[3];
+#pragma unroll
+      for (int n = 0; n < 3; ++n) page[n] = find_page(n);
+#pragma unroll
+      for (int n = 0; n < 3; ++n) where[n][tid % KEYS] = find_row(n, page[n]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < 3; ++n) where[n][tid % KEYS] = -1;
+    }
+    if (tid < 2 * (KEYS / 32)) odd_rows[tid / (KEYS / 32)][tid % (KEYS / 32)] = 0;
     __syncthreads();
-    if (begin + (n + 1) * KEYS > it.s.ctx) {
-      if (tid < KEYS / 32) odd_rows[n & 1][tid] = 0;
-      __syncthreads();
-    }
-    if (n + 2 < tiles) fetch(n + 2);
-  }
+    fetch(0);
+    stash(0);
+    fetch(1);
+    __syncthreads();
 
-  float* slot = nullptr;
-  if (it.splits > 1) {
-    if (it.slot >= max_slots) return;  // only where start is not ascending
-    slot = space(a).slots + (int64_t)it.slot * slot_floats<DP, ROWS>();
-  }
+    for (int n = 0; n < tiles; ++n) {
+      const int later = find_page(n + 3);
+      const uint16_t* kb = kt[n & 1];
+      const uint16_t* vb = vt[n & 1];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    float sum = l[r];
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    const int in_tile = (wave * RT + r) * 16 + col, row = row0 + r * 16 + col;
-    if (row >= rows) continue;
-    const float top = m[r] * c, base = m[r] == -INFINITY ? 0.f : top;
-    if (slot) {
+      for (int half = 0; half < KEYS / 32; ++half) {
+        const int key0 = begin + n * KEYS + half * 32;
+        const uint32_t there = (uint32_t)__ballot(where[n & 3][half * 32 + (lane & 31)] >= 0);
+        f32x4 sc[RT][2];
 #pragma unroll
-      for (int d = 0; d < OT; ++d) *reinterpret_cast<f32x4*>(slot + in_tile * DP + d * 16 + quad * 4) = o[r][d];
-      if (quad == 0) {
-        slot[ROWS * DP + in_tile] = top;
-        slot[ROWS * DP + ROWS + in_tile] = sum;
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) sc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const u32x4 kf = *reinterpret_cast<const u32x4*>(kb + (half * 32 + t * 16 + col) * KP + s * 32 + quad * 8);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) sc[r][t] = mfma16x16x32<DT>(kf, q[r][s], sc[r][t]);
+          }
+        if (key0 + 32 > it.s.ctx || there != 0xffffffffu) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) mask_scores(seen_bits(a, it, node[r], key0, there), quad, sc[r]);
+        }
+        u32x4 w[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[r] = weigh<DT, OT>(sc[r], c, m[r], l[r], o[r]);
+#pragma unroll
+        for (int d = 0; d < OT; ++d) {
+          const uint16_t* p = vb + (half * 32 + quad * 4 + (col >> 2)) * VP + d * 16 + (col & 3) * 4;
+          const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * VP);
+          const u32x4 vf = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+          for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf, w[r], o[r][d]);
+        }
+        uint32_t odd = odd_rows[n & 1][half];
+        while (odd) {
+          const int i = __ffs(odd) - 1;
+          odd &= odd - 1;
+          const uint16_t* p = vbase + where[n & 3][half * 32 + i];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, sc[r], o[r]);
+        }
       }
-      continue;
+      // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
+      // between two barriers, and only where there can be any.
+      if (n + 1 < tiles) stash(n + 1);
+      where[(n + 3) & 3][tid % KEYS] = find_row(n + 3, later);
+      __syncthreads();
+      if (begin + (n + 1) * KEYS > it.s.ctx) {
+        if (tid < KEYS / 32) odd_rows[n & 1][tid] = 0;
+        __syncthreads();
+      }
+      if (n + 2 < tiles) fetch(n + 2);
     }
-    const int t = it.s.q0 + row / group, h = it.h * group + row % group;
-    if (a.lse && quad == 0) a.lse[(int64_t)t * a.heads + h] = log_sum(base, sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+
+    float* slot = nullptr;
+    if (to - from < it.tiles)
+      slot = space(a).slots + (int64_t)slot_of(it.part, it.part_tiles, it.line) * slot_floats<DP, ROWS>();
 #pragma unroll
-    for (int d = 0; d < OT; ++d) store_quad<DT>(a, t, h, d * 16 + quad * 4, o[r][d], inv);
+    for (int r = 0; r < RT; ++r) {
+      float sum = l[r];
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      const int in_tile = (wave * RT + r) * 16 + col, row = row0 + r * 16 + col;
+      if (row >= rows) continue;
+      const float top = m[r] * c, base = m[r] == -INFINITY ? 0.f : top;
+      if (slot) {
+#pragma unroll
+        for (int d = 0; d < OT; ++d) *reinterpret_cast<f32x4*>(slot + in_tile * DP + d * 16 + quad * 4) = o[r][d];
+        if (quad == 0) {
+          slot[ROWS * DP + in_tile] = top;
+          slot[ROWS * DP + ROWS + in_tile] = sum;
+        }
+        continue;
+      }
+      const int t = it.s.q0 + row / group, h = it.h * group + row % group;
+      if (a.lse && quad == 0) a.lse[(int64_t)t * a.heads + h] = log_sum(base, sum);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+      for (int d = 0; d < OT; ++d) store_quad<DT>(a, t, h, d * 16 + quad * 4, o[r][d], inv);
+    }
+    if (it.line + it.tiles >= it.end) return;
+    next_line<ROWS, KEYS>(a, &it);
   }
 }
 
-// ---------------------------------------------------------------- join of runs
-// One block per row (token, head): wave w takes runs w, w + 4, ...; 64 lanes
-// hold the DP columns.
-template <int DT, int DP, int ROWS, int KEYS>
-__global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a, int max_slots) {
+// ---------------------------------------------------------------- join of pieces
+// A row (token, head) is joined by SHARE waves, wave w of them taking pieces w,
+// w + SHARE, ...; 64 lanes hold the DP columns.  SHARE = 4 (a block a row) while
+// the rows are few and their pieces many, else 1.
+template <int DT, int DP, int ROWS, int KEYS, int SHARE>
+__global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a) {
   constexpr int PER = DP / kWave;
   const Space sp = space(a);
-  const int t = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t out_row = (int64_t)blockIdx.x * (kWaves / SHARE) + (SHARE == 1 ? wave : 0);
+  if (out_row >= (int64_t)a.T * a.heads) return;
+  const int t = (int)(out_row / a.heads), head = (int)(out_row % a.heads);
   const int group = a.heads / a.kv_heads;
   // The sequence of token t.
   int b = -1;
@@ -691,18 +706,18 @@ __global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a, int max
     if (m) b = base + __ffsll((unsigned long long)m) - 1;
   }
   if (b < 0) return;
-  const int first = sp.first[b];
-  if (first < 0) return;
   const Seq s = sequence(a, b);
-  const int tiles = *sp.tiles;
-  const int splits = (key_tiles(s.len, KEYS) + tiles - 1) / tiles, rts = row_tiles(s.n, group, ROWS);
+  const int part_tiles = *sp.part;
+  const int tiles = key_tiles(s.len, KEYS), rts = row_tiles(s.n, group, ROWS);
   const int row = (t - s.q0) * group + head % group, rt = row / ROWS, in_tile = row % ROWS;
-  auto slot_of = [&](int split) {
-    const int64_t i = min((int64_t)first + ((int64_t)split * a.kv_heads + head / group) * rts + rt, (int64_t)max_slots - 1);
-    return sp.slots + i * slot_floats<DP, ROWS>();
+  const int line = sp.first[b] + (head / group * rts + rt) * tiles;
+  const int part0 = line / part_tiles, splits = min((line + tiles - 1) / part_tiles, kParts - 1) - part0 + 1;
+  if (splits < 2) return;
+  auto piece = [&](int i) {
+    return sp.slots + (int64_t)slot_of(part0 + i, part_tiles, line) * slot_floats<DP, ROWS>();
   };
   float top = -INFINITY;
-  for (int i = lane; i < splits; i += kWave) top = fmaxf(top, slot_of(i)[ROWS * DP + in_tile]);
+  for (int i = lane; i < splits; i += kWave) top = fmaxf(top, piece(i)[ROWS * DP + in_tile]);
 #pragma unroll
   for (int x = 1; x < kWave; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
   const float base = top == -INFINITY ? 0.f : top;
@@ -710,67 +725,73 @@ __global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a, int max
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = wave; i < splits; i += kWaves) {
-    const float* p = slot_of(i);
+  for (int i = SHARE == 1 ? 0 : wave; i < splits; i += SHARE) {
+    const float* p = piece(i);
     const float f = __builtin_amdgcn_exp2f(p[ROWS * DP + in_tile] - base);
     sum += f * p[ROWS * DP + ROWS + in_tile];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] += f * p[in_tile * DP + e * kWave + lane];
+    for (int e = 0; e < PER; ++e) acc[e] += f * p[in_tile * DP + lane * PER + e];
   }
-  __shared__ float part[kWaves][DP + 1];
+  if constexpr (SHARE > 1) {
+    __shared__ float part[kWaves][DP + 1];
 #pragma unroll
-  for (int e = 0; e < PER; ++e) part[wave][e * kWave + lane] = acc[e];
-  if (lane == 0) part[wave][DP] = sum;
-  __syncthreads();
-  sum = part[0][DP] + part[1][DP] + part[2][DP] + part[3][DP];
+    for (int e = 0; e < PER; ++e) part[wave][lane * PER + e] = acc[e];
+    if (lane == 0) part[wave][DP] = sum;
+    __syncthreads();
+    if (wave != 0) return;
+    sum = part[0][DP] + part[1][DP] + part[2][DP] + part[3][DP];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int c = lane * PER + e;
+      acc[e] = part[0][c] + part[1][c] + part[2][c] + part[3][c];
+    }
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int c = threadIdx.x; c < a.dim; c += kWaves * kWave)
-    a.out[t * a.out_token + head * a.out_head + c] =
-        (uint16_t)from_f32<DT>((part[0][c] + part[1][c] + part[2][c] + part[3][c]) * inv);
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(int64_t)t * a.heads + head] =
-        sum > 0.f ? (base + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : (sum == 0.f ? -INFINITY : sum);
+  uint16_t* out = a.out + t * a.out_token + head * a.out_head;
+#pragma unroll
+  for (int e = 0; e < PER; ++e)
+    if (lane * PER + e < a.dim) out[lane * PER + e] = (uint16_t)from_f32<DT>(acc[e] * inv);
+  if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads + head] = log_sum(base, sum);
 }
 
-// A launch takes WIDE kernels of 4 x 16 RT rows, or narrow ones of 16 RT.
-template <int DT, int DP, int RT, bool WIDE>
+// ROWS = 16: the kernel for few rows; 64, 128: the one for many.
+template <int DT, int DP, int ROWS>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
-  constexpr int ROWS = (WIDE ? kWaves : 1) * 16 * RT;
-  constexpr int KEYS = WIDE ? wide_tile<DP>() : kTile;
-  const int64_t rows = (int64_t)a.T * (a.heads / a.kv_heads);
-  // Every sequence has at most one row tile that is not full.
-  const int64_t tiles = rows / ROWS + (a.B < rows ? a.B : rows);
-  const unsigned grid = (unsigned)(kItems + tiles * a.kv_heads);
-  if constexpr (WIDE)
-    attention_rows_kernel<DT, DP, RT><<<grid, kWaves * kWave, 0, s>>>(a, kItems, 2 * kItems);
+  constexpr int KEYS = ROWS > 16 ? wide_tile<DP>() : kTile;
+  if constexpr (ROWS > 16)
+    attention_rows_kernel<DT, DP, ROWS / 64><<<kParts, kWaves * kWave, 0, s>>>(a);
   else
-    attention_kernel<DT, DP, RT><<<grid, kWaves * kWave, 0, s>>>(a, kItems, 2 * kItems);
+    attention_kernel<DT, DP><<<kParts, kWaves * kWave, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  join_kernel<DT, DP, ROWS, KEYS><<<(unsigned)(a.T * a.heads), kWaves * kWave, 0, s>>>(a, 2 * kItems);
+  const int64_t out_rows = (int64_t)a.T * a.heads;
+  if (out_rows <= kCus * 8)
+    join_kernel<DT, DP, ROWS, KEYS, kWaves><<<(unsigned)out_rows, kWaves * kWave, 0, s>>>(a);
+  else
+    join_kernel<DT, DP, ROWS, KEYS, 1><<<(unsigned)((out_rows + kWaves - 1) / kWaves), kWaves * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// Rows of a workgroup, from what an average sequence has: 16 or 32 in the
-// kernel whose waves split the positions, 64 or 128 in the one whose waves
-// split the rows.  256-wide heads leave registers for 16 and 64 only.
+// Rows of a line, from what an average sequence has.  16 rows: the waves split
+// the positions, which measured best there (64 sequences of one token, 8 rows
+// each: 124 us against 173 us with 64).  Above, the waves split the rows: 64
+// (two sequences of 32 rows on average over 120000 positions: 82 us against
+// 122 us with two row tiles whose waves split the positions) or 128.
+// 256-wide heads leave registers for 64 only.
 int choose_rows(int64_t B, int64_t T, int group, int dp) {
   const int64_t rows = (T * group + B - 1) / B;
-  if (rows <= 16) return 16;
-  if (dp == 256) return 64;
-  return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  return rows <= 16 ? 16 : rows <= 64 || dp == 256 ? 64 : 128;
 }
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 template <int DT, int DP>
 hipError_t launch_rows(const AttnArgs& a, int rows, hipStream_t s) {
-  if (rows == 16) return launch<DT, DP, 1, false>(a, s);
+  if (rows == 16) return launch<DT, DP, 16>(a, s);
   if constexpr (DP != 256) {
-    if (rows == 32) return launch<DT, DP, 2, false>(a, s);
-    if (rows == 128) return launch<DT, DP, 2, true>(a, s);
+    if (rows == 128) return launch<DT, DP, 128>(a, s);
   }
-  return launch<DT, DP, 1, true>(a, s);
+  return launch<DT, DP, 64>(a, s);
 }
 
 template <int DT>
@@ -784,7 +805,7 @@ hipError_t launch_dt(const AttnArgs& a, hipStream_t s) {
 
 size_t attention_workspace(int32_t B, int32_t T, int32_t heads, int32_t kv_heads, int32_t dim) {
   const int dp = padded_dim(dim), rows = choose_rows(B, T, heads / kv_heads, dp);
-  return (4 + ((size_t)B + 3) / 4 * 4 + (size_t)2 * kItems * rows * (dp + 2)) * 4;
+  return (4 + ((size_t)B + 3) / 4 * 4 + (size_t)2 * kParts * rows * (dp + 2)) * 4;
 }
 
 hipError_t launch_attention(const AttnArgs& args, int dtype, hipStream_t s) {
