@@ -172,11 +172,18 @@ __device__ __forceinline__ bool not_finite(u32x4 v) {
   return bad;
 }
 
-// Offset (elements) of position pos of the sequence whose table row is given,
-// -1 if no page of the cache holds it.  pos is below max_pages * page_size.
-__device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int page, int pos) {
-  return in_range(page, a.num_pages) ? page * a.kv_page + (int64_t)(pos - pos / a.page_size * a.page_size) * a.kv_token
-                                     : (int64_t)-1;
+// pos / page_size for 0 <= pos < 2^31: the high half of a product with
+// ceil(2^(31 + s) / page_size), s the bits of page_size - 1, shifted by s - 1.
+// The excess of the factor is below 1, so that of the quotient is below
+// 2^31 / 2^(31 + s) <= 1 / page_size, too little to reach the next whole number.
+__device__ __forceinline__ int page_of_position(const AttnArgs& a, int pos) {
+  return a.page_mul ? (int)(__umulhi((uint32_t)pos, a.page_mul) >> a.page_shift) : pos;
+}
+
+// Offset (elements) of position pos of the sequence in page `page`, the id that
+// its table row holds for page number w; -1 if that is no page of the cache.
+__device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int page, int w, int pos) {
+  return in_range(page, a.num_pages) ? page * a.kv_page + (pos - w * a.page_size) * a.kv_token : (int64_t)-1;
 }
 
 // Queries of one row tile as matrix-core operand: lane col holds row
@@ -347,10 +354,12 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
 #pragma unroll
     for (int d = 0; d < OT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // Page of position key0 + lane % 32, or -1.
-    auto page_of = [&](int key0) {
+    // Page of position key0 + lane % 32 (of the last one, where that is beyond
+    // the end), and the cache row that follows from it.
+    auto page_of = [&](int key0) { return table[page_of_position(a, min(key0 + (lane & 31), end - 1))]; };
+    auto row_of = [&](int key0, int page) {
       const int pos = key0 + (lane & 31);
-      return pos < end ? table[pos / a.page_size] : -1;
+      return pos < end ? cache_row(a, page, page_of_position(a, pos), pos) : (int64_t)-1;
     };
     u32x4 k[2][KS], v[VL];
     auto load = [&](int64_t safe) {
@@ -369,10 +378,14 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
     };
 
     int key0 = begin + wave * kKeys;
-    int page = page_of(key0);
-    int64_t at = cache_row(a, page, key0 + (lane & 31));
-    if (key0 < end) load(at < 0 ? 0 : at);
-    page = page_of(key0 + kTile);
+    int page = 0;
+    int64_t at = -1;
+    if (key0 < end) {
+      page = page_of(key0);
+      at = row_of(key0, page);
+      load(at < 0 ? 0 : at);
+      page = page_of(key0 + kTile);
+    }
     for (; key0 < end; key0 += kTile) {
       const uint32_t there = (uint32_t)__ballot(at >= 0);  // both halves of the wave agree
       const int64_t here = at < 0 ? 0 : at;
@@ -412,7 +425,7 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
 
       // The next step.
       const int next = key0 + kTile;
-      at = cache_row(a, page, next + (lane & 31));
+      at = row_of(next, page);
       if (next < end) load(at < 0 ? 0 : at);
       page = page_of(next + kTile);
 
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
   constexpr int PASS = KEYS / RPP;
   __shared__ __align__(16) uint16_t kt[2][KEYS * KP];
   __shared__ __align__(16) uint16_t vt[2][KEYS * VP];
-  __shared__ int64_t where[4][KEYS];         // cache rows of a tile's positions
+  __shared__ int64_t where[4][KEYS];         // cache rows of a tile's positions (0 where there is none)
   __shared__ uint32_t odd_rows[2][KEYS / 32];
 
   Place it;
@@ -510,6 +523,12 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
   const float c = exponent_scale(a);
   const int piece = tid % CPR * 8, prow = tid / CPR;
   const int clamped = piece < a.dim ? piece : a.dim - 8;
+  // Key columns beyond dim are never written again: they have to be finite.
+  if (a.dim < DP) {
+    for (int e = tid; e < KEYS * KP / 8; e += kWaves * kWave)
+      reinterpret_cast<u32x4*>(kt[0])[e] = reinterpret_cast<u32x4*>(kt[1])[e] = u32x4{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
 
   for (;;) {
     const int rows = it.s.n * group, row0 = it.rt * ROWS + wave * 16 * RT;
@@ -524,8 +543,9 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       node[r] = row / group;
       load_queries<DP>(a, it, node[r], it.h * group + row % group, quad, q[r]);
     }
-    const uint16_t* kbase = a.k + it.h * a.kv_head;
-    const uint16_t* vbase = a.v + it.h * a.kv_head;
+    const uint16_t* vhead = a.v + it.h * a.kv_head;
+    const uint16_t* kbase = a.k + it.h * a.kv_head + clamped;  // of this thread's pieces
+    const uint16_t* vbase = vhead + clamped;
     const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
 
     f32x4 o[RT][OT];
@@ -539,62 +559,69 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
     }
 
     u32x4 kreg[PASS], vreg[PASS];
-    bool absent[PASS];
-    // Page of a position of tile n (the one this thread looks up), and the cache
-    // row that follows from it.  The two are apart so that the page is on its
-    // way during a whole tile.
-    auto find_page = [&](int n) { return table[min(begin + n * KEYS + tid % KEYS, max(end - 1, 0)) / a.page_size]; };
-    auto find_row = [&](int n, int page) {
+    // Page of a position of tile n (each wave looks up all of them), and the
+    // cache row that follows from it.  The two are apart so that the page is on
+    // its way during a whole tile.
+    auto find_page = [&](int n) {
+      return table[page_of_position(a, min(begin + n * KEYS + tid % KEYS, max(end - 1, 0)))];
+    };
+    // Notes the cache rows of tile n; returns a bit for each that exists.
+    auto note_rows = [&](int n, int page) {
       const int pos = begin + n * KEYS + tid % KEYS;
-      return pos < end ? cache_row(a, page, pos) : (int64_t)-1;
+      const int64_t at = pos < end ? cache_row(a, page, page_of_position(a, pos), pos) : (int64_t)-1;
+      where[n & 3][tid % KEYS] = at < 0 ? 0 : at;
+      return (uint64_t)__ballot(at >= 0);
     };
     auto fetch = [&](int n) {
 #pragma unroll
       for (int i = 0; i < PASS; ++i) {
         const int64_t at = where[n & 3][prow + i * RPP];
-        absent[i] = at < 0;
-        kreg[i] = *reinterpret_cast<const u32x4*>(kbase + (at < 0 ? 0 : at) + clamped);
-        vreg[i] = *reinterpret_cast<const u32x4*>(vbase + (at < 0 ? 0 : at) + clamped);
+        kreg[i] = *reinterpret_cast<const u32x4*>(kbase + at);
+        vreg[i] = *reinterpret_cast<const u32x4*>(vbase + at);
       }
     };
-    // Tile n from the registers into its buffer.  A value row of a drafted node
-    // that is not finite is staged as 0 and noted.
-    auto stash = [&](int n) {
-      const bool drafted = begin + (n + 1) * KEYS > it.s.ctx;
+    // Tile n from the registers into its buffer.  Value rows that do not exist
+    // are staged as 0; so are those of drafted nodes that are not finite, which
+    // are noted.
+    auto stash = [&](int n, uint64_t there) {
+      const bool plain = begin + (n + 1) * KEYS <= it.s.ctx && (KEYS == 64 ? !~there : (uint32_t)there == ~0u);
+      if (!plain) {
 #pragma unroll
-      for (int i = 0; i < PASS; ++i) {
-        const int r = prow + i * RPP;
-        u32x4 x = vreg[i];
-        if (absent[i]) x = u32x4{0u, 0u, 0u, 0u};
-        *reinterpret_cast<u32x4*>(&kt[n & 1][r * KP + piece]) = piece < a.dim ? kreg[i] : u32x4{0u, 0u, 0u, 0u};
-        if (drafted) {
-          const uint64_t lanes = __ballot(not_finite<DT>(x));
-          const int first = lane / CPR * CPR;
-          if (lanes && ((lanes >> first) & ((1ull << CPR) - 1ull))) {
-            x = u32x4{0u, 0u, 0u, 0u};
-            if (lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
-          }
+        for (int i = 0; i < PASS; ++i) {
+          const int r = prow + i * RPP, first = lane / CPR * CPR;
+          const bool absent = !((there >> r) & 1);
+          const uint64_t lanes = __ballot(not_finite<DT>(vreg[i]) && !absent);
+          const bool odd = lanes && ((lanes >> first) & ((1ull << CPR) - 1ull));
+          if (odd && lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
+          if (absent || odd) vreg[i] = u32x4{0u, 0u, 0u, 0u};
         }
-        *reinterpret_cast<u32x4*>(&vt[n & 1][r * VP + piece]) = x;
+      }
+      if (piece < a.dim) {
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) {
+          *reinterpret_cast<u32x4*>(&kt[n & 1][(prow + i * RPP) * KP + piece]) = kreg[i];
+          *reinterpret_cast<u32x4*>(&vt[n & 1][(prow + i * RPP) * VP + piece]) = vreg[i];
+        }
       }
     };
 
     const int tiles = end > begin ? (end - begin + KEYS - 1) / KEYS : 0;
-    if (a.max_pages > 0) {
+    uint64_t there0 = 0, there1 = 0, there2 = 0;  // positions of tiles n, n + 1, n + 2
+    if (tid < 2 * (KEYS / 32)) odd_rows[tid / (KEYS / 32)][tid % (KEYS / 32)] = 0;
+    if (tiles > 0) {
       int page[3];
 #pragma unroll
       for (int n = 0; n < 3; ++n) page[n] = find_page(n);
-#pragma unroll
-      for (int n = 0; n < 3; ++n) where[n][tid % KEYS] = find_row(n, page[n]);
-    } else {
-#pragma unroll
-      for (int n = 0; n < 3; ++n) where[n][tid % KEYS] = -1;
+      there0 = note_rows(0, page[0]);
+      there1 = note_rows(1, page[1]);
+      there2 = note_rows(2, page[2]);
     }
-    if (tid < 2 * (KEYS / 32)) odd_rows[tid / (KEYS / 32)][tid % (KEYS / 32)] = 0;
     __syncthreads();
-    fetch(0);
-    stash(0);
-    fetch(1);
+    if (tiles > 0) {
+      fetch(0);
+      stash(0, there0);
+      fetch(1);
+    }
     __syncthreads();
 
     for (int n = 0; n < tiles; ++n) {
@@ -604,7 +631,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
 #pragma unroll
       for (int half = 0; half < KEYS / 32; ++half) {
         const int key0 = begin + n * KEYS + half * 32;
-        const uint32_t there = (uint32_t)__ballot(where[n & 3][half * 32 + (lane & 31)] >= 0);
+        const uint32_t there = (uint32_t)(there0 >> (half * 32));
         f32x4 sc[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -637,15 +664,17 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
         while (odd) {
           const int i = __ffs(odd) - 1;
           odd &= odd - 1;
-          const uint16_t* p = vbase + where[n & 3][half * 32 + i];
+          const uint16_t* p = vhead + where[n & 3][half * 32 + i];
 #pragma unroll
           for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, sc[r], o[r]);
         }
       }
       // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
       // between two barriers, and only where there can be any.
-      if (n + 1 < tiles) stash(n + 1);
-      where[(n + 3) & 3][tid % KEYS] = find_row(n + 3, later);
+      if (n + 1 < tiles) stash(n + 1, there1);
+      there0 = there1;
+      there1 = there2;
+      there2 = note_rows(n + 3, later);
       __syncthreads();
       if (begin + (n + 1) * KEYS > it.s.ctx) {
         if (tid < KEYS / 32) odd_rows[n & 1][tid] = 0;
@@ -813,6 +842,12 @@ hipError_t launch_attention(const AttnArgs& args, int dtype, hipStream_t s) {
   if (a.num_pages == 0) {  // nothing is there to be read: any legal address will do
     a.k = a.v = a.q;
     a.kv_head = 0;
+  }
+  a.page_mul = a.page_shift = 0;
+  if (a.page_size > 1) {
+    const int bits = 32 - __builtin_clz((uint32_t)(a.page_size - 1));
+    a.page_mul = (uint32_t)(((1ull << (31 + bits)) + a.page_size - 1) / a.page_size);
+    a.page_shift = bits - 1;
   }
   return dtype == 0 ? launch_dt<0>(a, s) : launch_dt<1>(a, s);
 }

@@ -95,6 +95,7 @@ struct AttnArgs {
   const uint16_t* v;
   int64_t kv_page, kv_token, kv_head;
   int32_t num_pages, page_size;
+  uint32_t page_mul, page_shift;  // set by the launcher: division by page_size
   const int32_t* table;
   int64_t ld_table;
   int32_t max_pages;
