@@ -13,6 +13,15 @@ using lora::ok;
 
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
+int check_workspace(const void* workspace, size_t given, size_t need, const char* fn) {
+  if (need > 0 && (!workspace || given < need))
+    return fail(LORA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? given : (size_t)0);
+  if (need > 0 && !aligned(workspace, 16))
+    return fail(LORA_ERR_WORKSPACE, "%s: workspace must be 16-byte aligned", fn);
+  return LORA_OK;
+}
+
 // ---------------------------------------------------------------- 4-bit products
 // Shape of a weight; LORA_OK if its packed form can exist.
 int check_q4(int32_t n, int32_t k, int32_t group, int dtype, const char* fn) {
@@ -57,15 +66,6 @@ int check_entries(int32_t n, const char* fn) {
   if (n < 0) return fail(LORA_ERR_INVALID_ARG, "%s: n %d < 0", fn, n);
   if (n > LORA_MAX_PAGE_ENTRIES)
     return fail(LORA_ERR_UNSUPPORTED, "%s: n %d above %d", fn, n, LORA_MAX_PAGE_ENTRIES);
-  return LORA_OK;
-}
-
-int check_workspace(const void* workspace, size_t given, size_t need, const char* fn) {
-  if (need > 0 && (!workspace || given < need))
-    return fail(LORA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
-                workspace ? given : (size_t)0);
-  if (need > 0 && !aligned(workspace, 16))
-    return fail(LORA_ERR_WORKSPACE, "%s: workspace must be 16-byte aligned", fn);
   return LORA_OK;
 }
 
@@ -118,8 +118,12 @@ int lora_q4_pack(const uint8_t* codes, int64_t ld_codes, const void* scales, int
                     fn);
 }
 
+size_t lora_q4_matmul_workspace_bytes(int32_t T, int32_t n, int32_t k) {
+  return T < 1 || n < 1 || k < 1 || n > 0x7fffffff - 16 || k > 0x7fffffff - 128 ? 0 : lora::q4_workspace(T, n, k);
+}
+
 int lora_q4_matmul(const void* x, int64_t ldx, const lora_q4_weight* w, int32_t T, void* y, int64_t ldy,
-                   int add_inputs, void* stream) {
+                   int add_inputs, void* workspace, size_t workspace_bytes, void* stream) {
   static const char* fn = "lora_q4_matmul";
   if (!w) return fail(LORA_ERR_INVALID_ARG, "%s: w is NULL", fn);
   if (int e = check_q4(w->n, w->k, w->group, w->dtype, fn)) return e;
@@ -130,11 +134,13 @@ int lora_q4_matmul(const void* x, int64_t ldx, const lora_q4_weight* w, int32_t 
   if (ldy < w->n) return fail(LORA_ERR_INVALID_ARG, "%s: ldy %lld < n %d", fn, (long long)ldy, w->n);
   if (T == 0) return ok();
   if (!x || !y) return fail(LORA_ERR_INVALID_ARG, "%s: x and y must not be NULL", fn);
+  if (T > 65535 * 128) return fail(LORA_ERR_UNSUPPORTED, "%s: T %d is too large", fn, T);
+  if (int e = check_workspace(workspace, workspace_bytes, lora::q4_workspace(T, w->n, w->k), fn)) return e;
   const bool x_vec = aligned(x, 16) && ldx % 8 == 0 && w->k % 8 == 0;
   const bool y_vec = aligned(y, 8) && ldy % 4 == 0 && w->n % 4 == 0;
   return hip_status(lora::launch_q4_matmul(static_cast<const uint16_t*>(x), ldx, w->packed, w->n, w->k, w->group,
                                            w->has_zeros != 0, T, static_cast<uint16_t*>(y), ldy, add_inputs ? 1 : 0,
-                                           w->dtype, x_vec, y_vec, static_cast<hipStream_t>(stream)),
+                                           w->dtype, x_vec, y_vec, workspace, static_cast<hipStream_t>(stream)),
                     fn);
 }
 

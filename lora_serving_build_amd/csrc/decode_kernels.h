@@ -36,6 +36,27 @@ inline Q4Layout q4_layout(int32_t n, int32_t k, int32_t group, bool zeros) {
   return l;
 }
 
+struct Q4Args {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint8_t* packed;
+  int64_t scales_at, zeros_at;  // zeros_at = 0: every zero is 8
+  int32_t n, k, tiles, blocks;
+  int32_t T;
+  uint16_t* y;
+  int64_t ldy;
+  int add;
+  float* partial;  // sums of the splits, [splits][T][16 tiles]
+  int x_vec;  // x rows are 16-byte aligned and k a multiple of 8
+  int y_vec;  // y rows of four outputs are 8-byte aligned and whole
+};
+
+hipError_t launch_q4_f16(const Q4Args& a, int sub, hipStream_t s);
+hipError_t launch_q4_bf16(const Q4Args& a, int sub, hipStream_t s);
+
+// Bytes of the splits' sums of a product (0: it does not split k).
+size_t q4_workspace(int32_t T, int32_t n, int32_t k);
+
 hipError_t launch_q4_pack(const uint8_t* codes, int64_t ld_codes, const uint16_t* scales, int64_t ld_scales,
                           const uint8_t* zeros, int64_t ld_zeros, int32_t n, int32_t k, int32_t group,
                           void* packed, hipStream_t s);
@@ -44,7 +65,7 @@ hipError_t launch_q4_pack(const uint8_t* codes, int64_t ld_codes, const uint16_t
 // 8-byte aligned, ldy and n are multiples of 4.
 hipError_t launch_q4_matmul(const uint16_t* x, int64_t ldx, const void* packed, int32_t n, int32_t k,
                             int32_t group, bool zeros, int32_t T, uint16_t* y, int64_t ldy, int add,
-                            int dtype, bool x_vec, bool y_vec, hipStream_t s);
+                            int dtype, bool x_vec, bool y_vec, void* workspace, hipStream_t s);
 
 // ---------------------------------------------------------------- pages
 constexpr int kMaxPageEntries = 2048;

@@ -1,0 +1,476 @@
+// Kernels of the products with 4-bit weights, and the choice between them.
+//
+//   y[t, c] (+)= sum_g s[c, g] sum_{h in g} (q[c, h] - z[c, g]) x[t, h]
+//
+// The matrix cores take 16 rows of codes against 16 tokens: a code becomes a
+// 16-bit number with two bit operations, so even one token is cheapest on
+// them (the other 15 columns are free, and no sum over lanes is left).
+//
+// Included by one source file for each type (q4_f16.hip, q4_bf16.hip).
+#pragma once
+
+#include <type_traits>
+
+#include "decode_kernels.h"
+#include "lora_device.h"
+
+namespace lora {
+namespace {
+
+// ---------------------------------------------------------------- codes to 16-bit numbers
+// The masks and exponents of q4_numbers.  v_and_or_b32 takes no literals and
+// one scalar operand: with the masks in scalar and the exponents in vector
+// registers it is one instruction; from constants the compiler makes two.
+template <int DT>
+struct Q4Bits {
+  uint32_t low, high, low_exp, high_exp;
+  __device__ __forceinline__ Q4Bits() {
+    low = 0x000f000fu;
+    high = 0x00f000f0u;
+    low_exp = DT == 0 ? 0x64006400u : 0x43004300u;
+    high_exp = 0x54005400u;
+    asm("" : "+s"(low), "+s"(high));
+    asm("" : "+v"(low_exp), "+v"(high_exp));
+  }
+};
+
+// The 8 codes of a dword as matrix-core operand elements.
+// binary16: a code in bits 0..3 under the exponent of 1024 reads 1024 + q, one
+// in bits 4..7 under the exponent of 64 reads 64 + q; a packed subtraction of
+// 1024 + z or 64 + z leaves q - z exactly.  lo, hi: those two in both halves.
+// bfloat16 has no packed subtraction: a code under the exponent of 128 reads
+// 128 + q, and the caller takes (128 + z) sum x away from the sum.
+template <int DT>
+__device__ __forceinline__ u32x4 q4_numbers(uint32_t d, const Q4Bits<DT>& k, f16x2 lo, f16x2 hi) {
+  if constexpr (DT == 0) {
+    const uint32_t e = d >> 8;
+    u32x4 r;
+    r.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (d & k.low) | k.low_exp) - lo);
+    r.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (d & k.high) | k.high_exp) - hi);
+    r.z = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (e & k.low) | k.low_exp) - lo);
+    r.w = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (e & k.high) | k.high_exp) - hi);
+    return r;
+  } else {
+    return u32x4{(d & k.low) | k.low_exp, ((d >> 4) & k.low) | k.low_exp, ((d >> 8) & k.low) | k.low_exp,
+                 ((d >> 12) & k.low) | k.low_exp};
+  }
+}
+
+// ---------------------------------------------------------------- scales, zeros, results
+// Codes of MT row tiles for one block of 128 inputs, with scales and zeros.
+template <int SUB, int MT>
+struct Q4Codes {
+  u32x4 codes[MT];
+  u32x2 scales[MT][SUB];
+  uint32_t zeros[MT][SUB];
+};
+
+template <int DT, int SUB, bool ZEROS, int MT>
+__device__ __forceinline__ void q4_load(const Q4Args& a, const int64_t (&unit0)[MT], int b, int lane,
+                                        Q4Codes<SUB, MT>* r) {
+  const int col = lane & 15, quad = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int64_t unit = unit0[m] + b;
+    r->codes[m] = reinterpret_cast<const u32x4*>(a.packed)[unit * 64 + lane];
+#pragma unroll
+    for (int g = 0; g < SUB; ++g) {
+      r->scales[m][g] = *reinterpret_cast<const u32x2*>(a.packed + a.scales_at + (unit * SUB + g) * 32 + quad * 8);
+      if constexpr (ZEROS) {
+        const uint8_t* z = a.packed + a.zeros_at + (unit * SUB + g) * 16;
+        r->zeros[m][g] = DT == 0 ? (uint32_t)z[col] : *reinterpret_cast<const uint32_t*>(z + quad * 4);
+      } else {
+        r->zeros[m][g] = DT == 0 ? 8u : 0x08080808u;
+      }
+    }
+  }
+}
+
+// A sub-group's scales as the results hold rows (4 quad + e), and what the
+// codes' zeros become: the operand rows' in binary16, the results' in bfloat16.
+template <int DT>
+struct Q4Scale {
+  f32x4 scale, base;
+  f16x2 z_lo, z_hi;
+};
+
+template <int DT>
+__device__ __forceinline__ Q4Scale<DT> q4_scale(u32x2 scales, uint32_t z) {
+  Q4Scale<DT> r;
+  float lo, hi;
+  unpack2<DT>(scales.x, &lo, &hi);
+  r.scale.x = lo;
+  r.scale.y = hi;
+  unpack2<DT>(scales.y, &lo, &hi);
+  r.scale.z = lo;
+  r.scale.w = hi;
+  if constexpr (DT == 0) {
+    r.base = f32x4{0.f, 0.f, 0.f, 0.f};
+    r.z_lo = __builtin_bit_cast(f16x2, 0x64006400u | z | (z << 16));
+    r.z_hi = __builtin_bit_cast(f16x2, 0x54005400u | (z << 4) | (z << 20));
+  } else {
+    r.z_lo = r.z_hi = f16x2{};
+    r.base = f32x4{128.f + (float)(z & 255u), 128.f + (float)((z >> 8) & 255u), 128.f + (float)((z >> 16) & 255u),
+                   128.f + (float)(z >> 24)};
+  }
+  return r;
+}
+
+// Outputs c .. c + 3 of token t (those below n).
+template <int DT>
+__device__ __forceinline__ void q4_store(const Q4Args& a, int t, int c, f32x4 r) {
+  uint16_t* y = a.y + (int64_t)t * a.ldy + c;
+  if (a.y_vec) {
+    if (c >= a.n) return;
+    if (a.add) {
+      const u32x2 old = *reinterpret_cast<const u32x2*>(y);
+      float p, q;
+      unpack2<DT>(old.x, &p, &q);
+      r.x += p;
+      r.y += q;
+      unpack2<DT>(old.y, &p, &q);
+      r.z += p;
+      r.w += q;
+    }
+    *reinterpret_cast<u32x2*>(y) = u32x2{cvt_pack2<DT>(r.x, r.y), cvt_pack2<DT>(r.z, r.w)};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < a.n) y[e] = (uint16_t)from_f32<DT>(r[e] + (a.add ? to_f32<DT>(y[e]) : 0.f));
+  }
+}
+
+// ---------------------------------------------------------------- product
+// For the fewest tokens: one workgroup takes MT row tiles and 16 tokens, the
+// blocks of k dealt out to its eight waves in turn; the waves' sums meet in LDS and
+// are added in wave order, so there is one launch and no workspace.  D of the
+// matrix core: lane l holds outputs 4 (l / 16) + 0..3 of token l % 16.
+constexpr int kWavesPerTile = 8;
+
+template <int DT, int SUB, bool ZEROS, int MT>
+__global__ void __launch_bounds__(kWavesPerTile* kWave) q4_kernel(Q4Args a) {
+  constexpr int W = kWavesPerTile;
+  __shared__ __align__(16) f32x4 sums[W][MT][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, quad = lane >> 4;
+  const int tile0 = blockIdx.x * MT;
+  const Q4Bits<DT> bits;
+  // Tokens beyond T read the last row; their columns are not stored.
+  const uint16_t* xr = a.x + (int64_t)(col < a.T ? col : a.T - 1) * a.ldx + quad * 8;
+  // Row tiles beyond the last read the last one; their rows are not stored.
+  int64_t unit0[MT];
+  f32x4 acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    unit0[m] = (int64_t)(tile0 + m < a.tiles ? tile0 + m : a.tiles - 1) * a.blocks;
+    acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  for (int b = wave; b < a.blocks; b += W) {
+    Q4Codes<SUB, MT> r;
+    q4_load<DT, SUB, ZEROS, MT>(a, unit0, b, lane, &r);
+    u32x4 x[4];
+    const int h = b * 128;
+    if (a.x_vec && h + 128 <= a.k) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[s] = *reinterpret_cast<const u32x4*>(xr + h + s * 32);
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[s] = load8_16<false>(xr + h + s * 32, a.k - quad * 8 - h - s * 32);
+    }
+#pragma unroll
+    for (int g = 0; g < SUB; ++g) {
+      f32x4 xs = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (DT == 1) {  // sums of x, in every row
+        const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+#pragma unroll
+        for (int s = g * (4 / SUB); s < (g + 1) * (4 / SUB); ++s) xs = mfma16x16x32<DT>(ones, x[s], xs);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const Q4Scale<DT> sc = q4_scale<DT>(r.scales[m][g], r.zeros[m][g]);
+        f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = g * (4 / SUB); s < (g + 1) * (4 / SUB); ++s)
+          part = mfma16x16x32<DT>(q4_numbers<DT>(r.codes[m][s], bits, sc.z_lo, sc.z_hi), x[s], part);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (DT == 1) part[e] = __builtin_fmaf(-sc.base[e], xs[e], part[e]);
+          acc[m][e] = __builtin_fmaf(sc.scale[e], part[e], acc[m][e]);
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int m = 0; m < MT; ++m) sums[wave][m][lane] = acc[m];
+  __syncthreads();
+  for (int o = threadIdx.x; o < MT * kWave; o += W * kWave) {
+    const int l = o & (kWave - 1), m = o / kWave;
+    f32x4 r = sums[0][m][l];
+#pragma unroll
+    for (int w = 1; w < W; ++w) r += sums[w][m][l];
+    if ((l & 15) < a.T) q4_store<DT>(a, l & 15, (tile0 + m) * 16 + (l >> 4) * 4, r);
+  }
+}
+
+// ---------------------------------------------------------------- product with shared x
+// For more than a few tokens x is read as often as the weight or more: each
+// row tile of codes (8 k bytes) meets 2 T k bytes of it.  Here the eight waves
+// of a workgroup take row tiles of their own (MT each) and share x through
+// LDS, in the order in which the matrix core takes it, double-buffered; the
+// next chunk's x is on its way in registers, the next block's codes too.  The
+// workgroups of one row group split k, and a second kernel adds their sums in
+// order.  The sums of x that a bfloat16 product needs are taken while x is
+// staged.
+constexpr int kShareWaves = 8;
+
+template <int DT, int SUB, bool ZEROS, int MT, int NT>
+__global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared_kernel(Q4Args a, int splits) {
+  constexpr int CB = NT >= 8 ? 1 : 8 / NT;  // blocks of a chunk: up to 32 KiB of x
+  constexpr int OPS = CB * NT * 4;          // operands of 16 tokens x 32 inputs
+  constexpr int MINE = (OPS + kShareWaves - 1) / kShareWaves;
+  __shared__ __align__(16) u32x4 xs[2][MINE * kShareWaves][kWave];
+  __shared__ float sums[DT == 1 ? 2 : 1][DT == 1 ? MINE * kShareWaves : 1][16];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, quad = lane >> 4;
+  const int tile0 = (blockIdx.x / splits * kShareWaves + wave) * MT, split = blockIdx.x % splits;
+  const int t0 = blockIdx.y * (16 * NT);
+  const int first = (int)((int64_t)a.blocks * split / splits), last = (int)((int64_t)a.blocks * (split + 1) / splits);
+  const Q4Bits<DT> bits;
+
+  int64_t unit0[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) unit0[m] = (int64_t)(tile0 + m < a.tiles ? tile0 + m : a.tiles - 1) * a.blocks;
+
+  // Operand f of a chunk: 16-token tile f / 4 % NT, step f % 4 of its block
+  // f / (4 NT).  This wave stages operands wave, wave + 8, ...; what lies beyond
+  // the split, or beyond the chunk's operands, is staged too and not used
+  // (nothing here is conditional: the compiler would move the loads into the
+  // conditions, where each waits for the one before).
+  u32x4 xreg[MINE];
+  auto fetch_as = [&](int chunk, auto vec) {
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+      const int f = wave + j * kShareWaves;
+      const int b = min(first + chunk * CB + f / (4 * NT), last - 1), t = t0 + f / 4 % NT * 16 + col;
+      const int h = b * 128 + f % 4 * 32 + quad * 8;
+      const uint16_t* row = a.x + (int64_t)(t < a.T ? t : a.T - 1) * a.ldx;
+      xreg[j] = vec ? load8_16_masked(row, h, a.k, true) : load8_16<false>(row + h, a.k - h);
+    }
+  };
+  auto fetch = [&](int chunk) {
+    if (a.x_vec)
+      fetch_as(chunk, std::true_type());
+    else
+      fetch_as(chunk, std::false_type());
+  };
+  auto stash = [&](int chunk) {
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+      const int f = wave + j * kShareWaves;
+      xs[chunk & 1][f][lane] = xreg[j];
+      if constexpr (DT == 1) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float lo, hi;
+          unpack2<DT>(xreg[j][e], &lo, &hi);
+          sum += lo + hi;
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        sums[chunk & 1][f][col] = sum;  // four lanes, one value
+      }
+    }
+  };
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  Q4Codes<SUB, MT> next;
+  fetch(0);
+  q4_load<DT, SUB, ZEROS, MT>(a, unit0, first, lane, &next);
+  stash(0);
+  fetch(1);
+  __syncthreads();
+  const int chunks = (last - first + CB - 1) / CB;
+  for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+      const int b = first + c * CB + cb;
+      if (b >= last) break;
+      const Q4Codes<SUB, MT> now = next;
+      q4_load<DT, SUB, ZEROS, MT>(a, unit0, min(b + 1, last - 1), lane, &next);
+#pragma unroll
+      for (int g = 0; g < SUB; ++g) {
+        f32x4 part[MT][NT];
+        Q4Scale<DT> sc[MT];
+        float total[NT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) sc[m] = q4_scale<DT>(now.scales[m][g], now.zeros[m][g]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          total[i] = 0.f;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) part[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int s = g * (4 / SUB); s < (g + 1) * (4 / SUB); ++s) {
+          u32x4 w[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) w[m] = q4_numbers<DT>(now.codes[m][s], bits, sc[m].z_lo, sc[m].z_hi);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const int f = (cb * NT + i) * 4 + s;
+            const u32x4 x = xs[c & 1][f][lane];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) part[m][i] = mfma16x16x32<DT>(w[m], x, part[m][i]);
+            if constexpr (DT == 1) total[i] += sums[c & 1][f][col];
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (DT == 1) part[m][i][e] = __builtin_fmaf(-sc[m].base[e], total[i], part[m][i][e]);
+              acc[m][i][e] = __builtin_fmaf(sc[m].scale[e], part[m][i][e], acc[m][i][e]);
+            }
+      }
+    }
+    if (c + 1 == chunks) break;
+    stash(c + 1);
+    fetch(c + 2);
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = (tile0 + m) * 16 + quad * 4;
+    if (tile0 + m >= a.tiles) continue;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = t0 + i * 16 + col;
+      if (t >= a.T) continue;
+      if (splits > 1)
+        *reinterpret_cast<f32x4*>(a.partial + ((int64_t)split * a.T + t) * (a.tiles * 16) + row) = acc[m][i];
+      else
+        q4_store<DT>(a, t, row, acc[m][i]);
+    }
+  }
+}
+
+// y from the sums of the splits, four outputs a thread.
+template <int DT>
+__global__ void __launch_bounds__(256) q4_add_kernel(Q4Args a, int splits) {
+  const int c = (blockIdx.y * 256 + threadIdx.x) * 4, t = blockIdx.x;
+  if (c >= a.n) return;
+  const int64_t width = (int64_t)a.tiles * 16;
+  const float* p = a.partial + t * width + c;
+  f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll 4
+  for (int s = 1; s < splits; ++s) sum += *reinterpret_cast<const f32x4*>(p + s * a.T * width);
+  q4_store<DT>(a, t, c, sum);
+}
+
+// ---------------------------------------------------------------- launch
+// How a product is run.
+struct Q4Plan {
+  bool shared;   // x through LDS, k split over workgroups
+  int mt, nt;    // row tiles of a wave, token tiles
+  int splits;
+};
+
+inline Q4Plan q4_plan(int32_t T, int32_t tiles, int32_t blocks) {
+  Q4Plan p;
+  // Row tiles of a workgroup without sharing: as many as leave one workgroup
+  // of eight waves for each CU.
+  p.shared = false;
+  p.nt = 1;
+  p.splits = 1;
+  p.mt = tiles >= 1024 ? 4 : tiles >= 512 ? 2 : 1;
+  if (T <= 16) {
+    // Without sharing, codes and x together arrive at the 9.5 TB/s or so that
+    // the L2s deliver; with it, codes at the 4.6 TB/s of memory, and a second
+    // launch with its sums costs 5 us.  Measured (bfloat16, 16 tokens): 8192
+    // outputs of 28672 inputs 38 us without, 33 with; 8192 x 8192 12.3 and
+    // 12.6; 28672 outputs of 8192 inputs 31 and 34; one token always without.
+    const double codes = (double)tiles * blocks * 1088, x = (double)(tiles / p.mt) * blocks * 256 * T;
+    p.shared = codes / 4.6e6 + 5 < (codes + x) / 9.5e6;
+    if (p.shared) p.mt = 2;
+  } else {
+    p.shared = true;
+    const int passes = (T + 127) / 128, per = ((T + passes - 1) / passes + 15) / 16;
+    p.nt = per <= 2 ? 2 : per <= 4 ? 4 : per <= 6 ? 6 : 8;
+    // Two row tiles a wave halve the LDS reads, which bound many tokens, but
+    // halve the waves too.  Measured with 64 / 128 tokens, 8192 x 8192: 25 / 55
+    // us with one, 24 / 39 with two; 4096 x 4096: 15 / 26 and 18 / 26.
+    p.mt = p.nt >= 4 && tiles >= 512 ? 2 : 1;
+  }
+  if (p.shared) {
+    // About one workgroup for each CU (a few more where two fit a CU), each
+    // with four blocks at least.
+    const int groups = (tiles + p.mt * kShareWaves - 1) / (p.mt * kShareWaves);
+    const int passes = (T + 16 * p.nt - 1) / (16 * p.nt);
+    const int want = p.nt <= 2 ? (320 + groups * passes - 1) / (groups * passes) : 256 / (groups * passes);
+    const int most = blocks / 4;
+    p.splits = want > most ? most : want;
+    if (p.splits < 1) p.splits = 1;
+  }
+  return p;
+}
+
+template <int DT, int SUB, bool ZEROS, int MT>
+hipError_t launch_tiles(const Q4Args& a, hipStream_t s) {
+  q4_kernel<DT, SUB, ZEROS, MT><<<(a.tiles + MT - 1) / MT, kWavesPerTile * kWave, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int DT, int SUB, bool ZEROS, int MT, int NT>
+hipError_t launch_shared(const Q4Args& a, int splits, hipStream_t s) {
+  const int groups = (a.tiles + MT * kShareWaves - 1) / (MT * kShareWaves);
+  const dim3 grid(groups * splits, (a.T + 16 * NT - 1) / (16 * NT));
+  q4_shared_kernel<DT, SUB, ZEROS, MT, NT><<<grid, kShareWaves * kWave, 0, s>>>(a, splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  q4_add_kernel<DT><<<dim3(a.T, (a.n + 1023) / 1024), 256, 0, s>>>(a, splits);
+  return hipGetLastError();
+}
+
+template <int DT, int SUB, bool ZEROS>
+hipError_t launch_plan(const Q4Args& a, hipStream_t s) {
+  const Q4Plan p = q4_plan(a.T, a.tiles, a.blocks);
+  if (!p.shared) {
+    if (p.mt == 4) return launch_tiles<DT, SUB, ZEROS, 4>(a, s);
+    if (p.mt == 2) return launch_tiles<DT, SUB, ZEROS, 2>(a, s);
+    return launch_tiles<DT, SUB, ZEROS, 1>(a, s);
+  }
+  switch (p.nt * 4 + p.mt) {
+    case 1 * 4 + 2: return launch_shared<DT, SUB, ZEROS, 2, 1>(a, p.splits, s);
+    case 2 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 2>(a, p.splits, s);
+    case 4 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 4>(a, p.splits, s);
+    case 4 * 4 + 2: return launch_shared<DT, SUB, ZEROS, 2, 4>(a, p.splits, s);
+    case 6 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 6>(a, p.splits, s);
+    case 6 * 4 + 2: return launch_shared<DT, SUB, ZEROS, 2, 6>(a, p.splits, s);
+    case 8 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 8>(a, p.splits, s);
+    default: return launch_shared<DT, SUB, ZEROS, 2, 8>(a, p.splits, s);
+  }
+}
+
+template <int DT>
+hipError_t launch_type(const Q4Args& a, int sub, hipStream_t s) {
+  if (a.zeros_at) {
+    if (sub == 1) return launch_plan<DT, 1, true>(a, s);
+    return sub == 2 ? launch_plan<DT, 2, true>(a, s) : launch_plan<DT, 4, true>(a, s);
+  }
+  if (sub == 1) return launch_plan<DT, 1, false>(a, s);
+  return sub == 2 ? launch_plan<DT, 2, false>(a, s) : launch_plan<DT, 4, false>(a, s);
+}
+
+}  // namespace
+}  // namespace lora

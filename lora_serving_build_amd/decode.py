@@ -15,6 +15,7 @@ import lora_serving_build_amd as _base
 
 __all__ = [
     "Q4Weight", "lora_q4_packed_bytes", "lora_q4_pack", "lora_q4_matmul",
+    "lora_q4_matmul_workspace_bytes",
     "lora_tree_attention", "lora_tree_attention_workspace_bytes",
     "PageCache", "lora_pages_resize", "lora_pages_append", "lora_pages_copy", "lora_pages_fork",
     "lora_pages_fork_workspace_bytes", "lora_pages_accept", "lora_pages_free", "lora_pages_compact",
@@ -90,7 +91,9 @@ def _declare(L) -> None:
     L.lora_q4_packed_bytes.argtypes = [i32, i32, i32, ci]
     L.lora_q4_packed_bytes.restype = sz
     L.lora_q4_pack.argtypes = [p, i64, p, i64, p, i64, i32, i32, i32, ci, p, sz, p, p]
-    L.lora_q4_matmul.argtypes = [p, i64, p, i32, p, i64, ci, p]
+    L.lora_q4_matmul_workspace_bytes.argtypes = [i32, i32, i32]
+    L.lora_q4_matmul_workspace_bytes.restype = sz
+    L.lora_q4_matmul.argtypes = [p, i64, p, i32, p, i64, ci, p, sz, p]
     L.lora_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     L.lora_tree_attention_workspace_bytes.restype = sz
     L.lora_tree_attention.argtypes = [p, i64, i64, p, p, i32, i32, i32, ctypes.c_float, p, i64, i64, p, p, sz, ci, p]
@@ -139,6 +142,11 @@ def _on_gpu(device, *tensors) -> None:
             raise ValueError("every tensor must be on the same GPU")
 
 
+def _workspace(t: torch.Tensor, nbytes: int, given: torch.Tensor | None):
+    ws = _base._workspace(t.device, nbytes) if given is None else given
+    return (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
+
+
 # ---------------------------------------------------------------- 4-bit products
 class Q4Weight:
     """A weight in the kernel's layout: the packed device buffer and the C
@@ -182,7 +190,12 @@ def lora_q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor 
     return w
 
 
-def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bool = False) -> torch.Tensor:
+def lora_q4_matmul_workspace_bytes(T: int, n: int, k: int) -> int:
+    return int(_base.lib().lora_q4_matmul_workspace_bytes(int(T), int(n), int(k)))
+
+
+def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bool = False,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y[t, :n] (+)= x[t, :k] . W for every row t of x (decode and
     verification batches); y is [T][n] in the weight's dtype, and is returned."""
     if x.dtype != w.dtype or y.dtype != w.dtype:
@@ -191,8 +204,10 @@ def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bo
     T = x.shape[0]
     if x.shape[1] != w.k or y.shape[1] != w.n or y.shape[0] < T:
         raise ValueError(f"x must be [T][{w.k}] and y [T][{w.n}]")
-    _on_gpu(w.packed.device, x, y)
-    _run(_base.lib().lora_q4_matmul(x.data_ptr(), ldx, w._ref, T, y.data_ptr(), ldy, int(add_inputs), _stream(x)))
+    _on_gpu(w.packed.device, x, y, workspace)
+    L = _base.lib()
+    ws, ws_bytes = _workspace(x, L.lora_q4_matmul_workspace_bytes(T, w.n, w.k), workspace)
+    _run(L.lora_q4_matmul(x.data_ptr(), ldx, w._ref, T, y.data_ptr(), ldy, int(add_inputs), ws, ws_bytes, _stream(x)))
     return y
 
 
@@ -202,11 +217,6 @@ def _int32(t: torch.Tensor, name: str, n: int | None = None) -> int:
     if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] < n):
         raise ValueError(f"{name} must be a contiguous int32 vector" + (f" of {n} entries" if n is not None else ""))
     return t.data_ptr()
-
-
-def _workspace(t: torch.Tensor, nbytes: int, given: torch.Tensor | None):
-    ws = _base._workspace(t.device, nbytes) if given is None else given
-    return (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
 
 
 def lora_tree_attention_workspace_bytes(B: int, T: int, heads: int, kv_heads: int, dim: int) -> int:

@@ -69,10 +69,10 @@ def test_q4_matmul_refusals():
     def call(**a):
         w = D._CQ4Weight(a.get("n", 16), a.get("k", 128), a.get("group", 128), 0, a.get("dtype", 0),
                          a.get("packed", FAKE))
-        return lib.lora_q4_matmul(a.get("x", FAKE), a.get("ldx", 128), ctypes.addressof(w), a.get("T", 4),
-                                  a.get("y", FAKE), a.get("ldy", 16), 0, None)
+        return lib.lora_q4_matmul(a.get("x", FAKE), a.get("ldx", a.get("k", 128)), ctypes.addressof(w), a.get("T", 4),
+                                  a.get("y", FAKE), a.get("ldy", 16), 0, a.get("ws", None), a.get("ws_bytes", 0), None)
 
-    _expect(lib.lora_q4_matmul(FAKE, 128, None, 4, FAKE, 16, 0, None), BAD, "w is NULL")
+    _expect(lib.lora_q4_matmul(FAKE, 128, None, 4, FAKE, 16, 0, None, 0, None), BAD, "w is NULL")
     _expect(call(packed=None), BAD, "lora_q4_pack")
     _expect(call(packed=FAKE + 4), BAD, "lora_q4_pack")
     _expect(call(dtype=7), BAD, "dtype")
@@ -81,7 +81,15 @@ def test_q4_matmul_refusals():
     _expect(call(ldx=127), BAD, "ldx")
     _expect(call(ldy=15), BAD, "ldy")
     _expect(call(x=None), BAD, "must not be NULL")
+    _expect(call(T=65535 * 128 + 1), UNS, "too large")
+    need = lsb.lora_q4_matmul_workspace_bytes(40, 16, 4096)
+    assert need > 0 and lsb.lora_q4_matmul_workspace_bytes(1, 16, 4096) == 0
+    _expect(call(T=40, k=4096, ws=FAKE, ws_bytes=need - 1), WS, "workspace")
+    _expect(call(T=40, k=4096), WS, "workspace")
+    _expect(call(T=40, k=4096, ws=FAKE + 8, ws_bytes=need), WS, "aligned")
     assert call(T=0) == lsb.LORA_OK
+    for sizes in ((0, 16, 128), (4, 0, 128), (4, 16, 0)):
+        assert lsb.lora_q4_matmul_workspace_bytes(*sizes) == 0
 
 
 def test_q4_binding_refusals():
