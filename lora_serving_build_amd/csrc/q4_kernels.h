@@ -413,13 +413,15 @@ inline Q4Plan q4_plan(int32_t T, int32_t tiles, int32_t blocks) {
     p.mt = p.nt >= 4 && tiles >= 512 ? 2 : 1;
   }
   if (p.shared) {
-    // About one workgroup for each CU (a few more where two fit a CU), each
-    // with four blocks at least.
-    const int groups = (tiles + p.mt * kShareWaves - 1) / (p.mt * kShareWaves);
-    const int passes = (T + 16 * p.nt - 1) / (16 * p.nt);
-    const int want = p.nt <= 2 ? (320 + groups * passes - 1) / (groups * passes) : 256 / (groups * passes);
-    const int most = blocks / 4;
-    p.splits = want > most ? most : want;
+    // As many workgroups as CUs at most, so that none gets a second one while
+    // others wait; where that leaves one split, two workgroups a CU if they fit
+    // (up to 32 tokens).  Each split has four blocks at least.  Measured with
+    // 512 row tiles, 16 tokens, k = 28672: 33 us with 8 splits (256
+    // workgroups), 42 with 10.
+    const int groups = (tiles + p.mt * kShareWaves - 1) / (p.mt * kShareWaves) * ((T + 16 * p.nt - 1) / (16 * p.nt));
+    int want = 256 / groups;
+    if (want <= 1 && p.nt <= 2) want = 512 / groups;
+    p.splits = want < blocks / 4 ? want : blocks / 4;
     if (p.splits < 1) p.splits = 1;
   }
   return p;
