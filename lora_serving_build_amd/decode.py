@@ -8,6 +8,7 @@ dtype codes and the current stream of torch tensors.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -86,6 +87,11 @@ class _CPageCache(ctypes.Structure):
     ]
 
 
+# The same two structs packed at once.
+_BATCH = struct.Struct("@iiPPPqi4xPqi4x").pack
+_LAYER = struct.Struct("@PPqqqii").pack
+
+
 def _declare(L) -> None:
     p, i32, i64, sz, ci = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     L.lora_q4_packed_bytes.argtypes = [i32, i32, i32, ci]
@@ -118,8 +124,11 @@ def _run(rc: int) -> None:
         raise _base.LoraError(rc, _base.lora_last_error())
 
 
-def _stream(t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+# The calls below are made many times in a decoding step, some of them shorter
+# on the GPU than here on the host: checks take the cheapest accessors
+# (get_device, identity of dtypes), structs are packed in one go.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_I32, _U8, _F32, _I64 = torch.int32, torch.uint8, torch.float32, torch.int64
 
 
 def _code(t: torch.Tensor, name: str) -> int:
@@ -136,15 +145,41 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _on_gpu(device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device != device):
-            raise ValueError("every tensor must be on the same GPU")
+def _gpu(*tensors) -> int:
+    """Index of the GPU that holds all of the tensors (None: not given)."""
+    at = tensors[0].get_device()
+    if at >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != at:
+                break
+        else:
+            return at
+    raise ValueError("every tensor must be on the same GPU")
 
 
-def _workspace(t: torch.Tensor, nbytes: int, given: torch.Tensor | None):
-    ws = _base._workspace(t.device, nbytes) if given is None else given
-    return (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
+def _int32(t: torch.Tensor, name: str, n: int) -> int:
+    """Address of a contiguous int32 vector of (at least) n entries."""
+    if t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries")
+    return t.data_ptr()
+
+
+def _count(t: torch.Tensor, name: str) -> int:
+    """Entries of a vector that sets how many a call has."""
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be a vector")
+    return t.numel()
+
+
+def _workspace(at: int, stream: int, nbytes: int, given: torch.Tensor | None):
+    """Address and size of a call's workspace: the one given, or the stream's."""
+    if given is None:
+        if nbytes == 0:
+            return None, 0
+        given = _base._ws_cache.get((at, stream))
+        if given is None or given.numel() < nbytes:
+            given = _base._workspace(torch.device("cuda", at), nbytes)
+    return given.data_ptr(), given.numel() * given.element_size()
 
 
 # ---------------------------------------------------------------- 4-bit products
@@ -181,9 +216,8 @@ def lora_q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor 
     need = lora_q4_packed_bytes(n, k, group, zeros is not None)
     packed = torch.empty(max(need, 16), dtype=torch.uint8, device=codes.device)
     w = Q4Weight(packed, n, k, group, zeros is not None, scales.dtype)
-    if need:  # a shape without a packed form is refused below, before any launch
-        _on_gpu(codes.device, codes, scales, zeros)
-    stream = _stream(codes) if codes.is_cuda else 0
+    # A shape without a packed form is refused below, before any launch.
+    stream = _raw_stream(_gpu(codes, scales, zeros)) if need else 0
     _run(_base.lib().lora_q4_pack(codes.data_ptr(), ldc, scales.data_ptr(), lds,
                                   zeros.data_ptr() if zeros is not None else None, ldz, n, k, group, code,
                                   packed.data_ptr(), packed.numel(), w._ref, stream))
@@ -198,27 +232,26 @@ def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bo
                    workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y[t, :n] (+)= x[t, :k] . W for every row t of x (decode and
     verification batches); y is [T][n] in the weight's dtype, and is returned."""
-    if x.dtype != w.dtype or y.dtype != w.dtype:
+    if x.dtype is not w.dtype or y.dtype is not w.dtype:
         raise TypeError("x and y must have the weight's dtype")
-    ldx, ldy = _rows(x, "x"), _rows(y, "y")
-    T = x.shape[0]
-    if x.shape[1] != w.k or y.shape[1] != w.n or y.shape[0] < T:
+    if x.dim() != 2 or y.dim() != 2:
+        raise ValueError("x and y must be 2-D tensors with contiguous rows")
+    (T, k), (rows, n), (ldx, x_in), (ldy, y_in) = x.shape, y.shape, x.stride(), y.stride()
+    if (x_in != 1 and k > 1) or (y_in != 1 and n > 1):
+        raise ValueError("x and y must be 2-D tensors with contiguous rows")
+    if k != w.k or n != w.n or rows < T:
         raise ValueError(f"x must be [T][{w.k}] and y [T][{w.n}]")
-    _on_gpu(w.packed.device, x, y, workspace)
+    if T <= 1:  # the stride of a lone row means nothing
+        ldx, ldy = max(ldx, k), max(ldy, n)
+    at = _gpu(w.packed, x, y, workspace)
+    stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(x, L.lora_q4_matmul_workspace_bytes(T, w.n, w.k), workspace)
-    _run(L.lora_q4_matmul(x.data_ptr(), ldx, w._ref, T, y.data_ptr(), ldy, int(add_inputs), ws, ws_bytes, _stream(x)))
+    ws, ws_bytes = _workspace(at, stream, L.lora_q4_matmul_workspace_bytes(T, n, k), workspace)
+    _run(L.lora_q4_matmul(x.data_ptr(), ldx, w._ref, T, y.data_ptr(), ldy, 1 if add_inputs else 0, ws, ws_bytes, stream))
     return y
 
 
 # ---------------------------------------------------------------- tree attention
-def _int32(t: torch.Tensor, name: str, n: int | None = None) -> int:
-    """Address of a contiguous int32 vector of (at least) n entries."""
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] < n):
-        raise ValueError(f"{name} must be a contiguous int32 vector" + (f" of {n} entries" if n is not None else ""))
-    return t.data_ptr()
-
-
 def lora_tree_attention_workspace_bytes(B: int, T: int, heads: int, kv_heads: int, dim: int) -> int:
     return int(_base.lib().lora_tree_attention_workspace_bytes(B, T, heads, kv_heads, dim))
 
@@ -236,38 +269,45 @@ def lora_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     node j of its sequence (None: node i sees nodes 0..i); lse float32
     [T][heads].  Returns out."""
     code = _code(q, "q")
-    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype:
+    dt = q.dtype
+    if k_cache.dtype is not dt or v_cache.dtype is not dt or out.dtype is not dt:
         raise TypeError("q, k_cache, v_cache and out must share a dtype")
-    if q.dim() != 3 or k_cache.dim() != 4 or out.shape != q.shape or v_cache.shape != k_cache.shape:
+    shape, cache_shape, strides = q.shape, k_cache.shape, k_cache.stride()
+    if len(shape) != 3 or len(cache_shape) != 4 or out.shape != shape or v_cache.shape != cache_shape:
         raise ValueError("q and out must be [T][heads][dim], k_cache and v_cache four-dimensional and alike")
-    T, heads, dim = q.shape
-    num_pages, page_size, kv_heads, kdim = k_cache.shape
-    page_st, token_st, head_st, one = k_cache.stride()
+    T, heads, dim = shape
+    num_pages, page_size, kv_heads, kdim = cache_shape
+    page_st, token_st, head_st, one = strides
     if head_major:
         page_size, kv_heads, token_st, head_st = kv_heads, page_size, head_st, token_st
-    if kdim != dim or one != 1 or v_cache.stride() != k_cache.stride() or q.stride(2) != 1 or out.stride(2) != 1:
+    (q_token, q_head, q_one), (o_token, o_head, o_one) = q.stride(), out.stride()
+    if kdim != dim or one != 1 or v_cache.stride() != strides or q_one != 1 or o_one != 1:
         raise ValueError("head dims must agree and be contiguous, k_cache and v_cache must have the same strides")
-    if table.dtype != torch.int32 or table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
+    if table.dtype is not _I32 or table.dim() != 2:
         raise ValueError("table must be an int32 [B][max_pages] tensor with contiguous rows")
-    B, max_pages = table.shape
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()):
+    (B, max_pages), (ld_table, table_in) = table.shape, table.stride()
+    if table_in != 1 and max_pages > 1:
+        raise ValueError("table must be an int32 [B][max_pages] tensor with contiguous rows")
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (T, heads) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [T][heads] tensor")
-    words, ld_mask, mask_ptr = 0, 0, None
+    words, ld_mask, mask_ptr = 0, 0, 0
     if mask is not None:
-        if mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] < T or (mask.stride(1) != 1 and mask.shape[1] > 1):
+        if mask.dtype is not _I64 or mask.dim() != 2:
             raise ValueError("mask must be an int64 [T][words] tensor with contiguous rows")
-        words, mask_ptr = mask.shape[1], mask.data_ptr()
-        ld_mask = max(mask.stride(0), words)
-    _on_gpu(q.device, q, k_cache, v_cache, table, ctx_len, start, out, mask, lse, workspace)
-    batch = _CTreeBatch(B, T, _int32(start, "start", B + 1), _int32(ctx_len, "ctx_len", B), table.data_ptr(),
-                        max(table.stride(0), max_pages), max_pages, mask_ptr, ld_mask, words)
-    layer = _CKvLayer(k_cache.data_ptr(), v_cache.data_ptr(), page_st, token_st, head_st, num_pages, page_size)
+        (mask_rows, words), (ld_mask, mask_in) = mask.shape, mask.stride()
+        if mask_rows < T or (mask_in != 1 and words > 1):
+            raise ValueError("mask must be an int64 [T][words] tensor with contiguous rows")
+        mask_ptr, ld_mask = mask.data_ptr(), max(ld_mask, words)
+    at = _gpu(q, k_cache, v_cache, table, ctx_len, start, out, mask, lse, workspace)
+    batch = _BATCH(B, T, _int32(start, "start", B + 1), _int32(ctx_len, "ctx_len", B), table.data_ptr(),
+                   max(ld_table, max_pages), max_pages, mask_ptr, ld_mask, words)
+    layer = _LAYER(k_cache.data_ptr(), v_cache.data_ptr(), page_st, token_st, head_st, num_pages, page_size)
+    stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(q, L.lora_tree_attention_workspace_bytes(B, T, heads, kv_heads, dim), workspace)
-    _run(L.lora_tree_attention(q.data_ptr(), q.stride(0), q.stride(1), ctypes.addressof(layer),
-                               ctypes.addressof(batch), heads, kv_heads, dim, scale, out.data_ptr(), out.stride(0),
-                               out.stride(1), lse.data_ptr() if lse is not None else None, ws, ws_bytes, code,
-                               _stream(q)))
+    ws, ws_bytes = _workspace(at, stream, L.lora_tree_attention_workspace_bytes(B, T, heads, kv_heads, dim), workspace)
+    _run(L.lora_tree_attention(q.data_ptr(), q_token, q_head, layer, batch, heads, kv_heads, dim, scale,
+                               out.data_ptr(), o_token, o_head, lse.data_ptr() if lse is not None else None, ws,
+                               ws_bytes, code, stream))
     return out
 
 
@@ -294,7 +334,7 @@ class PageCache:
         self.page_size, self.heads, self.dim, self.head_major = (b, a, dim, True) if head_major else (a, b, dim, False)
         max_seqs, max_pages = table.shape
         refs_ptr, len_ptr = _int32(refs, "refs", pages), _int32(seq_len, "seq_len", max_seqs)
-        _on_gpu(pool.device, pool, refs, table, seq_len)
+        _gpu(pool, refs, table, seq_len)
         self.pool, self.refs, self.table, self.seq_len = pool, refs, table, seq_len
         self.num_pages, self.max_pages = pages, max_pages
         self.c = _CPageCache(pool.data_ptr(), pool.stride(0) * 2, pool.stride(1) * 2,
@@ -309,28 +349,17 @@ class PageCache:
         return self.pool[2 * i], self.pool[2 * i + 1]
 
 
-def _entries(cache: PageCache, n: int | None, **vectors):
-    """Number of entries and the addresses of the int32 vectors (None stays)."""
-    out = []
-    for name, t in vectors.items():
-        if t is None:
-            out.append(None)
-            continue
-        if n is None:
-            n = t.shape[0] if t.dim() == 1 else -1
-        out.append(_int32(t, name, n))
-        if t.device != cache.pool.device:
-            raise ValueError("every tensor must be on the cache's GPU")
-    return n, *out
-
-
 def lora_pages_resize(cache: PageCache, seqs: torch.Tensor, lens: torch.Tensor | None = None,
                       extra: torch.Tensor | None = None, status: torch.Tensor | None = None) -> None:
     """Sets the sequences' lengths (lens; None: as they are) and makes their
     rows hold exactly the pages of length + extra tokens.  status (optional):
     PAGES_OK, PAGES_NO_SPACE or PAGES_BAD for each."""
-    n, ps, pl, pe, pt = _entries(cache, None, seqs=seqs, lens=lens, extra=extra, status=status)
-    _run(_base.lib().lora_pages_resize(cache._ref, ps, pl, pe, n, pt, _stream(seqs)))
+    n = _count(seqs, "seqs")
+    at = _gpu(cache.pool, seqs, lens, extra, status)
+    _run(_base.lib().lora_pages_resize(cache._ref, _int32(seqs, "seqs", n),
+                                       _int32(lens, "lens", n) if lens is not None else None,
+                                       _int32(extra, "extra", n) if extra is not None else None, n,
+                                       _int32(status, "status", n) if status is not None else None, _raw_stream(at)))
 
 
 def lora_pages_append(cache: PageCache, layer: int, k: torch.Tensor, v: torch.Tensor, seqs: torch.Tensor,
@@ -338,23 +367,28 @@ def lora_pages_append(cache: PageCache, layer: int, k: torch.Tensor, v: torch.Te
     """Stores new tokens' keys and values ([T][heads][dim] each) of one layer
     behind the sequences' cached tokens: rows start[i] .. start[i + 1] - 1 go to
     positions seq_len[seqs[i]] and on."""
-    if k.dtype != cache.pool.dtype or v.dtype != cache.pool.dtype:
+    dt = cache.pool.dtype
+    if k.dtype is not dt or v.dtype is not dt:
         raise TypeError("k and v must have the cache's dtype")
-    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (cache.heads, cache.dim) or k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("k and v must be [T][heads][dim] with contiguous head dims, as in the cache")
-    n = seqs.shape[0]
-    _, ps = _entries(cache, n, seqs=seqs)
-    _, pst = _entries(cache, n + 1, start=start)
-    _on_gpu(cache.pool.device, k, v)
-    _run(_base.lib().lora_pages_append(cache._ref, 2 * layer, 2 * layer + 1, k.data_ptr(), k.stride(0), k.stride(1),
-                                       v.data_ptr(), v.stride(0), v.stride(1), cache.heads, cache.dim, ps, pst, n,
-                                       k.shape[0], _stream(k)))
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or shape[1] != cache.heads or shape[2] != cache.dim:
+        raise ValueError("k and v must be [T][heads][dim], as in the cache")
+    (k_token, k_head, k_one), (v_token, v_head, v_one) = k.stride(), v.stride()
+    if k_one != 1 or v_one != 1:
+        raise ValueError("k and v must have contiguous head dims")
+    n = _count(seqs, "seqs")
+    at = _gpu(cache.pool, k, v, seqs, start)
+    _run(_base.lib().lora_pages_append(cache._ref, 2 * layer, 2 * layer + 1, k.data_ptr(), k_token, k_head,
+                                       v.data_ptr(), v_token, v_head, cache.heads, cache.dim, _int32(seqs, "seqs", n),
+                                       _int32(start, "start", n + 1), n, shape[0], _raw_stream(at)))
 
 
 def lora_pages_copy(cache: PageCache, src_pages: torch.Tensor, dst_pages: torch.Tensor) -> None:
     """Copies page src_pages[i] to page dst_pages[i] in every pool."""
-    n, ps, pd = _entries(cache, None, src_pages=src_pages, dst_pages=dst_pages)
-    _run(_base.lib().lora_pages_copy(cache._ref, ps, pd, n, _stream(src_pages)))
+    n = _count(src_pages, "src_pages")
+    at = _gpu(cache.pool, src_pages, dst_pages)
+    _run(_base.lib().lora_pages_copy(cache._ref, _int32(src_pages, "src_pages", n), _int32(dst_pages, "dst_pages", n),
+                                     n, _raw_stream(at)))
 
 
 def lora_pages_fork_workspace_bytes(n: int, max_pages: int) -> int:
@@ -366,10 +400,13 @@ def lora_pages_fork(cache: PageCache, src: torch.Tensor, dst: torch.Tensor, stat
     """Gives every sequence dst[i] the state that src[i] had before the call:
     full pages are shared, the last, partly filled one is copied, and what
     dst[i] held is released."""
-    n, ps, pd, pt = _entries(cache, None, src=src, dst=dst, status=status)
+    n = _count(src, "src")
+    at = _gpu(cache.pool, src, dst, status, workspace)
+    stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(src, L.lora_pages_fork_workspace_bytes(n, cache.max_pages), workspace)
-    _run(L.lora_pages_fork(cache._ref, ps, pd, n, pt, ws, ws_bytes, _stream(src)))
+    ws, ws_bytes = _workspace(at, stream, L.lora_pages_fork_workspace_bytes(n, cache.max_pages), workspace)
+    _run(L.lora_pages_fork(cache._ref, _int32(src, "src", n), _int32(dst, "dst", n), n,
+                           _int32(status, "status", n) if status is not None else None, ws, ws_bytes, stream))
 
 
 def lora_pages_accept(cache: PageCache, seqs: torch.Tensor, drafted: torch.Tensor, path: torch.Tensor,
@@ -377,19 +414,25 @@ def lora_pages_accept(cache: PageCache, seqs: torch.Tensor, drafted: torch.Tenso
     """Moves the accepted nodes' rows (path int32 [n][columns], accepted[i] of
     them) to the front of each sequence's drafted rows, in every pool.  new_len
     receives seq_len + the rows kept; a resize with it makes that the length."""
-    n, ps, pd, pa, pn = _entries(cache, None, seqs=seqs, drafted=drafted, accepted=accepted, new_len=new_len)
-    if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] < n or (path.stride(1) != 1 and path.shape[1] > 1):
+    n = _count(seqs, "seqs")
+    if path.dtype is not _I32 or path.dim() != 2:
         raise ValueError("path must be an int32 [n][columns] tensor with contiguous rows")
-    _on_gpu(cache.pool.device, path)
-    _run(_base.lib().lora_pages_accept(cache._ref, ps, pd, path.data_ptr(), max(path.stride(0), path.shape[1]),
-                                       path.shape[1], pa, n, pn, _stream(seqs)))
+    (rows, columns), (ld_path, path_in) = path.shape, path.stride()
+    if rows < n or (path_in != 1 and columns > 1):
+        raise ValueError("path must be an int32 [n][columns] tensor with contiguous rows")
+    at = _gpu(cache.pool, seqs, drafted, path, accepted, new_len)
+    _run(_base.lib().lora_pages_accept(cache._ref, _int32(seqs, "seqs", n), _int32(drafted, "drafted", n),
+                                       path.data_ptr(), max(ld_path, columns), columns,
+                                       _int32(accepted, "accepted", n), n, _int32(new_len, "new_len", n),
+                                       _raw_stream(at)))
     return new_len
 
 
 def lora_pages_free(cache: PageCache, seqs: torch.Tensor) -> None:
     """Releases every page of the sequences."""
-    n, ps = _entries(cache, None, seqs=seqs)
-    _run(_base.lib().lora_pages_free(cache._ref, ps, n, _stream(seqs)))
+    n = _count(seqs, "seqs")
+    at = _gpu(cache.pool, seqs)
+    _run(_base.lib().lora_pages_free(cache._ref, _int32(seqs, "seqs", n), n, _raw_stream(at)))
 
 
 def lora_pages_compact_workspace_bytes(num_pages: int) -> int:
@@ -399,8 +442,9 @@ def lora_pages_compact_workspace_bytes(num_pages: int) -> int:
 def lora_pages_compact(cache: PageCache, live: torch.Tensor, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Moves the live pages to the lowest ids, in every pool and table row;
     live[0] receives their number."""
-    _, pl = _entries(cache, 1, live=live)
+    at = _gpu(cache.pool, live, workspace)
+    stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(live, L.lora_pages_compact_workspace_bytes(cache.num_pages), workspace)
-    _run(L.lora_pages_compact(cache._ref, pl, ws, ws_bytes, _stream(live)))
+    ws, ws_bytes = _workspace(at, stream, L.lora_pages_compact_workspace_bytes(cache.num_pages), workspace)
+    _run(L.lora_pages_compact(cache._ref, _int32(live, "live", 1), ws, ws_bytes, stream))
     return live

@@ -279,3 +279,14 @@ def test_page_cache_binding_refusals():
         lsb.PageCache(pool, refs, table.long(), lens)
     with pytest.raises(ValueError):
         lsb.PageCache(pool, refs, table, lens)                     # not on a GPU
+
+
+def test_packed_structs_match_the_header():
+    """The binding packs two structs in one go: their layout is that of C."""
+    import struct
+    assert struct.calcsize("@iiPPPqi4xPqi4x") == ctypes.sizeof(D._CTreeBatch)
+    assert struct.calcsize("@PPqqqii") == ctypes.sizeof(D._CKvLayer)
+    b = D._CTreeBatch.from_buffer_copy(D._BATCH(1, 2, 3, 4, 5, 6, 7, 8, 9, 10))
+    assert [getattr(b, f) for f, _ in b._fields_] == list(range(1, 11))
+    k = D._CKvLayer.from_buffer_copy(D._LAYER(1, 2, 3, 4, 5, 6, 7))
+    assert [getattr(k, f) for f, _ in k._fields_] == list(range(1, 8))
