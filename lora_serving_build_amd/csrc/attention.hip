@@ -45,14 +45,20 @@ __device__ __forceinline__ int key_tiles(int len, int keys) { return max((len + 
 // Number of parts: the workgroups that are resident at once.
 constexpr int kParts = kCus * 2;
 
+// What a line costs besides its tiles, in tiles: its start (pages, first keys,
+// queries) and end are not hidden.  Parts are equal in cost, so that those of
+// many short lines do not end last.
+template <int ROWS>
+constexpr int line_cost() { return ROWS > 16 ? 3 : 1; }
+
 // Positions of a tile that the waves share (what two workgroups' LDS holds).
 template <int DP>
 constexpr int wide_tile() { return DP == 256 ? 32 : 64; }
 
-// Workspace: the tiles of a part and the first tile of each sequence's lines (a
-// line after the other: key heads, row tiles running fastest), then two slots
-// for each part: a line cut by the part's start leaves its sums in the first,
-// one cut by its end only in the second.
+// Workspace: the cost of a part and of a line besides its tiles, and where each sequence's lines start (a line
+// after the other: key heads, row tiles running fastest; a line's cost comes
+// before its tiles), then two slots for each part: a line cut by the part's
+// start leaves its sums in the first, one cut by its end only in the second.
 struct Space {
   int32_t* part;
   int32_t* first;
@@ -71,15 +77,16 @@ __device__ __forceinline__ Space space(const AttnArgs& a) {
 template <int DP, int ROWS>
 constexpr int slot_floats() { return ROWS * (DP + 2); }
 
-__device__ __forceinline__ int slot_of(int part, int part_tiles, int line) {
-  return 2 * part + (line <= part * part_tiles ? 0 : 1);
+// tiles0: where the line's tiles start.
+__device__ __forceinline__ int slot_of(int part, int part_cost, int tiles0) {
+  return 2 * part + (tiles0 <= part * part_cost ? 0 : 1);
 }
 
 struct Place {
   Seq s;
   int b, h, rt, rts, tiles;  // sequence, key head, row tile of rts, tiles of the line
-  int line, at, end;         // first tile of the line, this piece's tiles (all from the call's start)
-  int part, part_tiles;
+  int line, at, end;         // start of the line, of this piece and end of the part (costs from the call's start)
+  int part, part_cost, cost;  // cost of a line besides its tiles
 };
 
 __device__ __forceinline__ void enter_sequence(const AttnArgs& a, int rows, int keys, int b, Place* p) {
@@ -97,28 +104,43 @@ __device__ __forceinline__ void enter_sequence(const AttnArgs& a, int rows, int 
 // it by itself from the lengths (prefix sums over the sequences), so there is
 // no plan to keep.  Neighbouring parts, whose lines often read the same keys,
 // go to one XCD and its L2.
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int COST>
 __device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
   const int lane = threadIdx.x & (kWave - 1);
   const int group = a.heads / a.kv_heads;
   const int part = (blockIdx.x & 7) * (kParts / 8) + (blockIdx.x >> 3);
-  auto tiles_of = [&](int b) {
-    if (b >= a.B) return 0;
-    const Seq s = sequence(a, b);
-    return row_tiles(s.n, group, ROWS) * a.kv_heads * key_tiles(s.len, KEYS);
-  };
-  uint32_t total = 0;
-  for (int base = 0; base < a.B; base += kWave)
-    total += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(tiles_of(base + lane)), kWave - 1);
-  const int part_tiles = max((int)((total + kParts - 1) / kParts), 1);
+  auto lines_of = [&](const Seq& s) { return row_tiles(s.n, group, ROWS) * a.kv_heads; };
+  uint32_t lines = 0, tiles = 0;
+  for (int base = 0; base < a.B; base += kWave) {
+    int l = 0, t = 0;
+    if (base + lane < a.B) {
+      const Seq s = sequence(a, base + lane);
+      l = lines_of(s);
+      t = l * key_tiles(s.len, KEYS);
+    }
+    lines += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(l), kWave - 1);
+    tiles += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(t), kWave - 1);
+  }
+  // With fewer tiles than parts every tile is a part.
+  const int cost = tiles <= (uint32_t)kParts ? 0 : COST;
+  const uint32_t total = tiles + lines * cost;
+  const int part_cost = max((int)((total + kParts - 1) / kParts), cost + 1);
+  p->cost = cost;
   p->part = part;
-  p->part_tiles = part_tiles;
-  p->at = part * part_tiles;
-  p->end = min((int)total, p->at + part_tiles);
-  if (part == 0 && threadIdx.x == 0) *space(a).part = part_tiles;
+  p->part_cost = part_cost;
+  p->at = part * part_cost;
+  p->end = min((int)total, p->at + part_cost);
+  if (part == 0 && threadIdx.x == 0) {
+    space(a).part[0] = part_cost;
+    space(a).part[1] = cost;
+  }
   int before = 0, b = -1, start = 0;
   for (int base = 0; base < a.B; base += kWave) {
-    const int mine = tiles_of(base + lane);
+    int mine = 0;
+    if (base + lane < a.B) {
+      const Seq s = sequence(a, base + lane);
+      mine = lines_of(s) * (cost + key_tiles(s.len, KEYS));
+    }
     const int end = before + wave_inclusive_sum(mine);
     if (part == 0 && threadIdx.x < kWave && base + lane < a.B) space(a).first[base + lane] = end - mine;
     const uint64_t m = __ballot(p->at < end && p->at >= end - mine);
@@ -132,17 +154,17 @@ __device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
   }
   if (b < 0 || p->at >= p->end) return false;
   enter_sequence(a, ROWS, KEYS, b, p);
-  const int line = (p->at - start) / p->tiles;
+  const int line = (p->at - start) / (cost + p->tiles);
   p->h = line / p->rts;
   p->rt = line % p->rts;
-  p->line = start + line * p->tiles;
+  p->line = start + line * (cost + p->tiles);
   return true;
 }
 
 // The line after the one of *p, in a part that goes on.
 template <int ROWS, int KEYS>
 __device__ __forceinline__ void next_line(const AttnArgs& a, Place* p) {
-  p->line += p->tiles;
+  p->line += p->cost + p->tiles;
   p->at = p->line;
   if (++p->rt < p->rts) return;
   p->rt = 0;
@@ -328,7 +350,7 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
   __shared__ float row_max[kWaves][ROWS], row_sum[kWaves][ROWS];
 
   Place it;
-  if (!find_part<ROWS, kTile>(a, &it)) return;
+  if (!find_part<ROWS, kTile, line_cost<ROWS>()>(a, &it)) return;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, quad = lane >> 4;
   const int group = a.heads / a.kv_heads;
@@ -338,7 +360,8 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
 
   for (;;) {
     const int rows = it.s.n * group, row0 = it.rt * ROWS;
-    const int from = it.at - it.line, to = min(it.tiles, it.end - it.line);
+    const int from = max(it.at - it.line - it.cost, 0), to = min(it.tiles, it.end - it.line - it.cost);
+    if (to > from) {
     const int begin = from * kTile, end = min(it.s.len, to * kTile);
 
     const int my_row = min(row0 + col, rows - 1);  // rows beyond the last read the last one
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
     __syncthreads();
     float* slot = nullptr;
     if (to - from < it.tiles)
-      slot = space(a).slots + (int64_t)slot_of(it.part, it.part_tiles, it.line) * slot_floats<DP, ROWS>();
+      slot = space(a).slots + (int64_t)slot_of(it.part, it.part_cost, it.line + it.cost) * slot_floats<DP, ROWS>();
     for (int e = threadIdx.x; e < ROWS * DP / 4; e += kWaves * kWave) {
       const int i = e / (DP / 4), cc = e % (DP / 4) * 4, row = row0 + i;
       if (row >= rows) continue;
@@ -491,7 +514,8 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
       if (a.lse && cc == 0) a.lse[(int64_t)t * a.heads + h] = log_sum(base, sum);
       store_quad<DT>(a, t, h, cc, x, sum == 0.f ? 0.f : 1.f / sum);
     }
-    if (it.line + it.tiles >= it.end) return;
+    }
+    if (it.line + it.cost + it.tiles >= it.end) return;
     __syncthreads();
     next_line<ROWS, kTile>(a, &it);
   }
@@ -516,7 +540,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
   __shared__ uint32_t odd_rows[2][KEYS / 32];
 
   Place it;
-  if (!find_part<ROWS, KEYS>(a, &it)) return;
+  if (!find_part<ROWS, KEYS, line_cost<ROWS>()>(a, &it)) return;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int col = lane & 15, quad = lane >> 4;
   const int group = a.heads / a.kv_heads;
@@ -532,7 +556,8 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
 
   for (;;) {
     const int rows = it.s.n * group, row0 = it.rt * ROWS + wave * 16 * RT;
-    const int from = it.at - it.line, to = min(it.tiles, it.end - it.line);
+    const int from = max(it.at - it.line - it.cost, 0), to = min(it.tiles, it.end - it.line - it.cost);
+    if (to > from) {
     const int begin = from * KEYS, end = min(it.s.len, to * KEYS);
 
     u32x4 q[RT][KS];
@@ -558,7 +583,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       for (int d = 0; d < OT; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    u32x4 kreg[PASS], vreg[PASS];
+    u32x4 reg[PASS];  // a tile's keys during its first half, its values after that
     // Page of a position of tile n (each wave looks up all of them), and the
     // cache row that follows from it.  The two are apart so that the page is on
     // its way during a whole tile.
@@ -572,36 +597,35 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       where[n & 3][tid % KEYS] = at < 0 ? 0 : at;
       return (uint64_t)__ballot(at >= 0);
     };
-    auto fetch = [&](int n) {
+    // Tile n's keys and values on their way into the registers, and from there
+    // into its buffer.  Value rows that do not exist are staged as 0; so are
+    // those of drafted nodes that are not finite, which are noted.
+    auto fetch = [&](int n, const uint16_t* base) {
 #pragma unroll
-      for (int i = 0; i < PASS; ++i) {
-        const int64_t at = where[n & 3][prow + i * RPP];
-        kreg[i] = *reinterpret_cast<const u32x4*>(kbase + at);
-        vreg[i] = *reinterpret_cast<const u32x4*>(vbase + at);
+      for (int i = 0; i < PASS; ++i) reg[i] = *reinterpret_cast<const u32x4*>(base + where[n & 3][prow + i * RPP]);
+    };
+    auto stash_keys = [&](int n) {
+      if (piece < a.dim) {
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) *reinterpret_cast<u32x4*>(&kt[n & 1][(prow + i * RPP) * KP + piece]) = reg[i];
       }
     };
-    // Tile n from the registers into its buffer.  Value rows that do not exist
-    // are staged as 0; so are those of drafted nodes that are not finite, which
-    // are noted.
-    auto stash = [&](int n, uint64_t there) {
+    auto stash_values = [&](int n, uint64_t there) {
       const bool plain = begin + (n + 1) * KEYS <= it.s.ctx && (KEYS == 64 ? !~there : (uint32_t)there == ~0u);
       if (!plain) {
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
           const int r = prow + i * RPP, first = lane / CPR * CPR;
           const bool absent = !((there >> r) & 1);
-          const uint64_t lanes = __ballot(not_finite<DT>(vreg[i]) && !absent);
+          const uint64_t lanes = __ballot(not_finite<DT>(reg[i]) && !absent);
           const bool odd = lanes && ((lanes >> first) & ((1ull << CPR) - 1ull));
           if (odd && lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
-          if (absent || odd) vreg[i] = u32x4{0u, 0u, 0u, 0u};
+          if (absent || odd) reg[i] = u32x4{0u, 0u, 0u, 0u};
         }
       }
       if (piece < a.dim) {
 #pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-          *reinterpret_cast<u32x4*>(&kt[n & 1][(prow + i * RPP) * KP + piece]) = kreg[i];
-          *reinterpret_cast<u32x4*>(&vt[n & 1][(prow + i * RPP) * VP + piece]) = vreg[i];
-        }
+        for (int i = 0; i < PASS; ++i) *reinterpret_cast<u32x4*>(&vt[n & 1][(prow + i * RPP) * VP + piece]) = reg[i];
       }
     };
 
@@ -618,9 +642,11 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
     }
     __syncthreads();
     if (tiles > 0) {
-      fetch(0);
-      stash(0, there0);
-      fetch(1);
+      fetch(0, kbase);
+      stash_keys(0);
+      fetch(0, vbase);
+      stash_values(0, there0);
+      fetch(1, kbase);
     }
     __syncthreads();
 
@@ -628,23 +654,45 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       const int later = find_page(n + 3);
       const uint16_t* kb = kt[n & 1];
       const uint16_t* vb = vt[n & 1];
+      // A wave whose rows all lie beyond the line's only helps with the staging.
+      // In each half tile all key operands are read before the products that take
+      // them, all value operands before the softmax: left to itself the compiler
+      // reads each when it is due and waits for LDS every time.
 #pragma unroll
       for (int half = 0; half < KEYS / 32; ++half) {
+        if (half == KEYS / 32 - 1) {  // the next tile's keys are there: its values' turn
+          stash_keys(n + 1);
+          fetch(n + 1, vbase);
+        }
+        if (row0 >= rows) continue;
         const int key0 = begin + n * KEYS + half * 32;
         const uint32_t there = (uint32_t)(there0 >> (half * 32));
+        u32x4 kf[2][KS];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+            kf[t][s] = *reinterpret_cast<const u32x4*>(kb + (half * 32 + t * 16 + col) * KP + s * 32 + quad * 8);
+        __builtin_amdgcn_sched_barrier(0);
         f32x4 sc[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int t = 0; t < 2; ++t) sc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            const u32x4 kf = *reinterpret_cast<const u32x4*>(kb + (half * 32 + t * 16 + col) * KP + s * 32 + quad * 8);
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int r = 0; r < RT; ++r) sc[r][t] = mfma16x16x32<DT>(kf, q[r][s], sc[r][t]);
-          }
+            for (int r = 0; r < RT; ++r) sc[r][t] = mfma16x16x32<DT>(kf[t][s], q[r][s], sc[r][t]);
+        u32x4 vf[OT];
+#pragma unroll
+        for (int d = 0; d < OT; ++d) {
+          const uint16_t* p = vb + (half * 32 + quad * 4 + (col >> 2)) * VP + d * 16 + (col & 3) * 4;
+          const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * VP);
+          vf[d] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        }
+        __builtin_amdgcn_sched_barrier(0);
         if (key0 + 32 > it.s.ctx || there != 0xffffffffu) {
 #pragma unroll
           for (int r = 0; r < RT; ++r) mask_scores(seen_bits(a, it, node[r], key0, there), quad, sc[r]);
@@ -653,13 +701,9 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
 #pragma unroll
         for (int r = 0; r < RT; ++r) w[r] = weigh<DT, OT>(sc[r], c, m[r], l[r], o[r]);
 #pragma unroll
-        for (int d = 0; d < OT; ++d) {
-          const uint16_t* p = vb + (half * 32 + quad * 4 + (col >> 2)) * VP + d * 16 + (col & 3) * 4;
-          const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * VP);
-          const u32x4 vf = {lo.x, lo.y, hi.x, hi.y};
+        for (int d = 0; d < OT; ++d)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf, w[r], o[r][d]);
-        }
+          for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf[d], w[r], o[r][d]);
         uint32_t odd = odd_rows[n & 1][half];
         while (odd) {
           const int i = __ffs(odd) - 1;
@@ -671,7 +715,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       }
       // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
       // between two barriers, and only where there can be any.
-      if (n + 1 < tiles) stash(n + 1, there1);
+      stash_values(n + 1, there1);
       there0 = there1;
       there1 = there2;
       there2 = note_rows(n + 3, later);
@@ -680,12 +724,12 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
         if (tid < KEYS / 32) odd_rows[n & 1][tid] = 0;
         __syncthreads();
       }
-      if (n + 2 < tiles) fetch(n + 2);
+      fetch(n + 2, kbase);
     }
 
     float* slot = nullptr;
     if (to - from < it.tiles)
-      slot = space(a).slots + (int64_t)slot_of(it.part, it.part_tiles, it.line) * slot_floats<DP, ROWS>();
+      slot = space(a).slots + (int64_t)slot_of(it.part, it.part_cost, it.line + it.cost) * slot_floats<DP, ROWS>();
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       float sum = l[r];
@@ -709,7 +753,8 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
 #pragma unroll
       for (int d = 0; d < OT; ++d) store_quad<DT>(a, t, h, d * 16 + quad * 4, o[r][d], inv);
     }
-    if (it.line + it.tiles >= it.end) return;
+    }
+    if (it.line + it.cost + it.tiles >= it.end) return;
     next_line<ROWS, KEYS>(a, &it);
   }
 }
@@ -736,14 +781,14 @@ __global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a) {
   }
   if (b < 0) return;
   const Seq s = sequence(a, b);
-  const int part_tiles = *sp.part;
+  const int part_cost = sp.part[0], cost = sp.part[1];
   const int tiles = key_tiles(s.len, KEYS), rts = row_tiles(s.n, group, ROWS);
   const int row = (t - s.q0) * group + head % group, rt = row / ROWS, in_tile = row % ROWS;
-  const int line = sp.first[b] + (head / group * rts + rt) * tiles;
-  const int part0 = line / part_tiles, splits = min((line + tiles - 1) / part_tiles, kParts - 1) - part0 + 1;
+  const int tiles0 = sp.first[b] + (head / group * rts + rt) * (cost + tiles) + cost;
+  const int part0 = tiles0 / part_cost, splits = min((tiles0 + tiles - 1) / part_cost, kParts - 1) - part0 + 1;
   if (splits < 2) return;
   auto piece = [&](int i) {
-    return sp.slots + (int64_t)slot_of(part0 + i, part_tiles, line) * slot_floats<DP, ROWS>();
+    return sp.slots + (int64_t)slot_of(part0 + i, part_cost, tiles0) * slot_floats<DP, ROWS>();
   };
   float top = -INFINITY;
   for (int i = lane; i < splits; i += kWave) top = fmaxf(top, piece(i)[ROWS * DP + in_tile]);
