@@ -42,6 +42,9 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
 __device__ __forceinline__ int row_tiles(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
 __device__ __forceinline__ int key_tiles(int len, int keys) { return max((len + keys - 1) / keys, 1); }
 
+// Positions of a table up to which lines are not cut: four steps of eight waves.
+constexpr int kShortLine = 4 * 8 * kKeys;
+
 // Number of parts: the workgroups that are resident at once.
 constexpr int kParts = kCus * 2;
 
@@ -159,6 +162,32 @@ __device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
   p->rt = line % p->rts;
   p->line = start + line * (cost + p->tiles);
   return true;
+}
+
+// Line number blockIdx.x, whole, as a part of its own; false if there are fewer.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ bool find_line(const AttnArgs& a, Place* p) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int group = a.heads / a.kv_heads, line = blockIdx.x;
+  int before = 0;
+  for (int base = 0; base < a.B; base += kWave) {
+    int mine = 0;
+    if (base + lane < a.B) mine = row_tiles(sequence(a, base + lane).n, group, ROWS) * a.kv_heads;
+    const int end = before + wave_inclusive_sum(mine);
+    const uint64_t m = __ballot(line < end && line >= end - mine);
+    if (m) {
+      const int f = __ffsll((unsigned long long)m) - 1;
+      enter_sequence(a, ROWS, KEYS, base + f, p);
+      const int at = line - __builtin_amdgcn_readlane(end - mine, f);
+      p->h = at / p->rts;
+      p->rt = at % p->rts;
+      p->line = p->at = p->part = p->cost = 0;
+      p->end = p->part_cost = p->tiles;
+      return true;
+    }
+    before = __builtin_amdgcn_readlane(end, kWave - 1);
+  }
+  return false;
 }
 
 // The line after the one of *p, in a part that goes on.
@@ -333,10 +362,12 @@ __device__ __forceinline__ void store_quad(const AttnArgs& a, int t, int h, int 
 // Waves of a workgroup take different positions.  Keys go from memory straight
 // into the matrix core's operand; values pass through the wave's own part of
 // LDS, which turns rows into columns.  The next step's keys and values are on
-// their way while this one's are used.
-template <int DT, int DP>
-__global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a) {
-  constexpr int ROWS = 16;
+// their way while this one's are used.  WHOLE: a workgroup takes one line, for
+// contexts so short that nothing needs to be cut and joined; else one of the
+// call's equal parts.
+template <int DT, int DP, int W, bool WHOLE>
+__global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a) {
+  constexpr int ROWS = 16, TILE = W * kKeys;
   constexpr int KS = DP / 32;             // matrix-core steps of a score
   constexpr int OT = DP / 16;             // tiles of the output's columns
   constexpr int PITCH = DP + 16;          // of a staged value row, in elements: rows start 8 banks apart
@@ -346,11 +377,11 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
   constexpr int JP = DP + 4;              // pitch of a row of sums
   constexpr int STAGE = kKeys * PITCH * 2;  // bytes of one wave's values
   constexpr int JOIN = ROWS * JP * 4;       // bytes of one wave's sums
-  __shared__ __align__(16) uint8_t lds[kWaves * (STAGE > JOIN ? STAGE : JOIN)];
-  __shared__ float row_max[kWaves][ROWS], row_sum[kWaves][ROWS];
+  __shared__ __align__(16) uint8_t lds[W * (STAGE > JOIN ? STAGE : JOIN)];
+  __shared__ float row_max[W][ROWS], row_sum[W][ROWS];
 
   Place it;
-  if (!find_part<ROWS, kTile, line_cost<ROWS>()>(a, &it)) return;
+  if (WHOLE ? !find_line<ROWS, TILE>(a, &it) : !find_part<ROWS, TILE, line_cost<ROWS>()>(a, &it)) return;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, quad = lane >> 4;
   const int group = a.heads / a.kv_heads;
@@ -362,7 +393,7 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
     const int rows = it.s.n * group, row0 = it.rt * ROWS;
     const int from = max(it.at - it.line - it.cost, 0), to = min(it.tiles, it.end - it.line - it.cost);
     if (to > from) {
-    const int begin = from * kTile, end = min(it.s.len, to * kTile);
+    const int begin = from * TILE, end = min(it.s.len, to * TILE);
 
     const int my_row = min(row0 + col, rows - 1);  // rows beyond the last read the last one
     const int node = my_row / group;
@@ -407,9 +438,9 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
       page = page_of(key0);
       at = row_of(key0, page);
       load(at < 0 ? 0 : at);
-      page = page_of(key0 + kTile);
+      page = page_of(key0 + TILE);
     }
-    for (; key0 < end; key0 += kTile) {
+    for (; key0 < end; key0 += TILE) {
       const uint32_t there = (uint32_t)__ballot(at >= 0);  // both halves of the wave agree
       const int64_t here = at < 0 ? 0 : at;
 
@@ -447,10 +478,10 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
       // The next step.
-      const int next = key0 + kTile;
+      const int next = key0 + TILE;
       at = row_of(next, page);
       if (next < end) load(at < 0 ? 0 : at);
-      page = page_of(next + kTile);
+      page = page_of(next + TILE);
 
       if (drafted || there != 0xffffffffu) mask_scores(seen_bits(a, it, node, key0, there), quad, sc);
       const u32x4 w = weigh<DT, OT>(sc, c, m, l, o);
@@ -487,17 +518,17 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
     float* slot = nullptr;
     if (to - from < it.tiles)
       slot = space(a).slots + (int64_t)slot_of(it.part, it.part_cost, it.line + it.cost) * slot_floats<DP, ROWS>();
-    for (int e = threadIdx.x; e < ROWS * DP / 4; e += kWaves * kWave) {
+    for (int e = threadIdx.x; e < ROWS * DP / 4; e += W * kWave) {
       const int i = e / (DP / 4), cc = e % (DP / 4) * 4, row = row0 + i;
       if (row >= rows) continue;
       float top = row_max[0][i];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, row_max[w][i]);
+      for (int w = 1; w < W; ++w) top = fmaxf(top, row_max[w][i]);
       const float base = top == -INFINITY ? 0.f : top;
       float sum = 0.f;
       f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float f = __builtin_amdgcn_exp2f(row_max[w][i] - base);
         sum += f * row_sum[w][i];
         x += *reinterpret_cast<const f32x4*>(join + (w * ROWS + i) * JP + cc) * f;
@@ -515,9 +546,9 @@ __global__ void __launch_bounds__(kWaves* kWave, DP == 256 ? 1 : 2) attention_ke
       store_quad<DT>(a, t, h, cc, x, sum == 0.f ? 0.f : 1.f / sum);
     }
     }
-    if (it.line + it.cost + it.tiles >= it.end) return;
+    if (WHOLE || it.line + it.cost + it.tiles >= it.end) return;
     __syncthreads();
-    next_line<ROWS, kTile>(a, &it);
+    next_line<ROWS, TILE>(a, &it);
   }
 }
 
@@ -873,7 +904,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
   if constexpr (ROWS > 16)
     attention_rows_kernel<DT, DP, ROWS / 64><<<kParts, kWaves * kWave, 0, s>>>(a);
   else
-    attention_kernel<DT, DP><<<kParts, kWaves * kWave, 0, s>>>(a);
+    attention_kernel<DT, DP, kWaves, false><<<kParts, kWaves * kWave, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t out_rows = (int64_t)a.T * a.heads;
@@ -881,6 +912,21 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
     join_kernel<DT, DP, ROWS, KEYS, kWaves><<<(unsigned)out_rows, kWaves * kWave, 0, s>>>(a);
   else
     join_kernel<DT, DP, ROWS, KEYS, 1><<<(unsigned)((out_rows + kWaves - 1) / kWaves), kWaves * kWave, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Whether the table holds so few positions that a workgroup of eight waves takes
+// each line whole: 509 positions, one token, 32 heads: 8.7 us and 3.9 us of the
+// join's launch in parts.
+bool short_lines(const AttnArgs& a) { return (int64_t)a.max_pages * a.page_size <= kShortLine; }
+
+template <int DT, int DP>
+hipError_t launch_short(const AttnArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.T * (a.heads / a.kv_heads);
+  // Every sequence has at most one row tile that is not full.
+  const int64_t lines = (rows / 16 + (a.B < rows ? a.B : rows)) * a.kv_heads;
+  constexpr int W = DP == 256 ? 4 : 8;  // what the registers allow
+  attention_kernel<DT, DP, W, true><<<(unsigned)lines, W * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -899,7 +945,7 @@ int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 template <int DT, int DP>
 hipError_t launch_rows(const AttnArgs& a, int rows, hipStream_t s) {
-  if (rows == 16) return launch<DT, DP, 16>(a, s);
+  if (rows == 16) return short_lines(a) ? launch_short<DT, DP>(a, s) : launch<DT, DP, 16>(a, s);
   if constexpr (DP != 256) {
     if (rows == 128) return launch<DT, DP, 128>(a, s);
   }
