@@ -792,18 +792,17 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
 
 // ---------------------------------------------------------------- join of pieces
 // A row (token, head) is joined by SHARE waves, wave w of them taking pieces w,
-// w + SHARE, ...; 64 lanes hold the DP columns.  SHARE = 4 (a block a row) while
-// the rows are few and their pieces many, else 1; up to kFew pieces are then
-// read at once, which leaves one memory latency behind the look-ups (48 nodes x
-// 16 sequences x 64 heads: 28 us piece by piece).
-constexpr int kFew = 4;
-
+// w + SHARE, ...; 64 lanes hold the DP columns.  SHARE = 8 (a block a row) while
+// the rows are few and their pieces many, else 1.  A wave reads a batch of pieces
+// at once, with a running maximum and sum over the batches, so that few memory
+// latencies follow the look-ups (48 nodes x 16 sequences x 64 heads: 28 us piece
+// by piece, 24 in batches).
 template <int DT, int DP, int ROWS, int KEYS, int SHARE>
-__global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a) {
+__global__ void __launch_bounds__((SHARE == 1 ? kWaves : SHARE) * kWave) join_kernel(AttnArgs a) {
   constexpr int PER = DP / kWave;
   const Space sp = space(a);
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t out_row = (int64_t)blockIdx.x * (kWaves / SHARE) + (SHARE == 1 ? wave : 0);
+  const int64_t out_row = SHARE == 1 ? (int64_t)blockIdx.x * kWaves + wave : (int64_t)blockIdx.x;
   if (out_row >= (int64_t)a.T * a.heads) return;
   const int t = (int)(out_row / a.heads), head = (int)(out_row % a.heads);
   const int group = a.heads / a.kv_heads;
@@ -825,70 +824,69 @@ __global__ void __launch_bounds__(kWaves* kWave) join_kernel(AttnArgs a) {
   auto piece = [&](int i) {
     return sp.slots + (int64_t)slot_of(part0 + i, part_cost, tiles0) * slot_floats<DP, ROWS>();
   };
+  constexpr int BATCH = SHARE == 1 ? 4 : 12;
   float top = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  auto values = [&](const float* p, float (&v)[PER]) {
-    if constexpr (PER == 1) {
-      v[0] = p[in_tile * DP + lane];
-    } else {
-      typedef float Vec __attribute__((ext_vector_type(PER)));
-      const Vec x = *reinterpret_cast<const Vec*>(p + in_tile * DP + lane * PER);
+  for (int i0 = SHARE == 1 ? 0 : wave; i0 < splits; i0 += SHARE * BATCH) {
+    float m[BATCH], l[BATCH], v[BATCH][PER];
 #pragma unroll
-      for (int e = 0; e < PER; ++e) v[e] = x[e];
-    }
-  };
-  float base;
-  if (SHARE == 1 && splits <= kFew) {
-    float m[kFew], l[kFew], v[kFew][PER];
-#pragma unroll
-    for (int i = 0; i < kFew; ++i) {
-      const float* p = piece(min(i, splits - 1));
+    for (int i = 0; i < BATCH; ++i) {  // pieces beyond the last: the last one, with no weight
+      const float* p = piece(min(i0 + i * SHARE, splits - 1));
       m[i] = p[ROWS * DP + in_tile];
       l[i] = p[ROWS * DP + ROWS + in_tile];
-      values(p, v[i]);
+      if constexpr (PER == 1) {
+        v[i][0] = p[in_tile * DP + lane];
+      } else {
+        typedef float Vec __attribute__((ext_vector_type(PER)));
+        const Vec x = *reinterpret_cast<const Vec*>(p + in_tile * DP + lane * PER);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[i][e] = x[e];
+      }
     }
+    float now = top;
 #pragma unroll
-    for (int i = 0; i < kFew; ++i) top = fmaxf(top, m[i]);
-    base = top == -INFINITY ? 0.f : top;
+    for (int i = 0; i < BATCH; ++i) now = fmaxf(now, m[i]);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float shrink = __builtin_amdgcn_exp2f(top - base);
+    sum *= shrink;
 #pragma unroll
-    for (int i = 0; i < kFew; ++i) {
-      if (i >= splits) continue;
+    for (int e = 0; e < PER; ++e) acc[e] *= shrink;
+    top = now;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (i0 + i * SHARE >= splits) continue;
       const float f = __builtin_amdgcn_exp2f(m[i] - base);
       sum += f * l[i];
 #pragma unroll
       for (int e = 0; e < PER; ++e) acc[e] += f * v[i][e];
     }
-  } else {
-    for (int i = lane; i < splits; i += kWave) top = fmaxf(top, piece(i)[ROWS * DP + in_tile]);
-#pragma unroll
-    for (int x = 1; x < kWave; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
-    base = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-    for (int i = SHARE == 1 ? 0 : wave; i < splits; i += SHARE) {
-      const float* p = piece(i);
-      const float f = __builtin_amdgcn_exp2f(p[ROWS * DP + in_tile] - base);
-      float v[PER];
-      values(p, v);
-      sum += f * p[ROWS * DP + ROWS + in_tile];
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] += f * v[e];
-    }
   }
   if constexpr (SHARE > 1) {
-    __shared__ float part[kWaves][DP + 1];
+    __shared__ float part[SHARE][DP + 2];
 #pragma unroll
     for (int e = 0; e < PER; ++e) part[wave][lane * PER + e] = acc[e];
-    if (lane == 0) part[wave][DP] = sum;
+    if (lane == 0) {
+      part[wave][DP] = sum;
+      part[wave][DP + 1] = top;
+    }
     __syncthreads();
     if (wave != 0) return;
-    sum = part[0][DP] + part[1][DP] + part[2][DP] + part[3][DP];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const int c = lane * PER + e;
-      acc[e] = part[0][c] + part[1][c] + part[2][c] + part[3][c];
+    for (int w = 1; w < SHARE; ++w) top = fmaxf(top, part[w][DP + 1]);
+    const float base = top == -INFINITY ? 0.f : top;
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < SHARE; ++w) {
+      const float f = __builtin_amdgcn_exp2f(part[w][DP + 1] - base);
+      sum += f * part[w][DP];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] += f * part[w][lane * PER + e];
     }
   }
+  const float base = top == -INFINITY ? 0.f : top;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t* out = a.out + t * a.out_token + head * a.out_head;
 #pragma unroll
@@ -909,7 +907,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   const int64_t out_rows = (int64_t)a.T * a.heads;
   if (out_rows <= kCus * 8)
-    join_kernel<DT, DP, ROWS, KEYS, kWaves><<<(unsigned)out_rows, kWaves * kWave, 0, s>>>(a);
+    join_kernel<DT, DP, ROWS, KEYS, 8><<<(unsigned)out_rows, 8 * kWave, 0, s>>>(a);
   else
     join_kernel<DT, DP, ROWS, KEYS, 1><<<(unsigned)((out_rows + kWaves - 1) / kWaves), kWaves * kWave, 0, s>>>(a);
   return hipGetLastError();
