@@ -61,17 +61,17 @@ int lora_q4_pack(const uint8_t *codes, int64_t ld_codes, const void *scales, int
                  const uint8_t *zeros, int64_t ld_zeros, int32_t n, int32_t k, int32_t group,
                  int dtype, void *packed, size_t packed_bytes, lora_q4_weight *w, void *stream);
 
-/* The product for T tokens.  Meant for decode and verification batches: the
- * weight is read from memory once for every 128 tokens.
+/* The product for T tokens.  Meant for decode and verification batches: a
+ * weight beyond the caches is read from memory once for every 128 tokens.
  *   x  [T][ldx], ldx >= k;  y  [T][ldy], ldy >= n; both of the weight's dtype;
  *   x and y must not overlap
- *   workspace  lora_q4_matmul_workspace_bytes(T, n, k) bytes (0 for most batches
- *              of up to 16 tokens, then NULL will do), 16-byte aligned, needs no
+ *   workspace  lora_q4_matmul_workspace_bytes(T, n, k, group) bytes (0 for most
+ *              batches of up to 16 tokens, then NULL will do), 16-byte aligned, needs no
  *              initialisation; calls that run concurrently must not share it
  * Same inputs give the same bits.
  * Errors: INVALID_ARG (NULL, T < 0, strides, a weight struct that no
- * lora_q4_pack filled), UNSUPPORTED (T above 65535 x 128), WORKSPACE, HIP. */
-size_t lora_q4_matmul_workspace_bytes(int32_t T, int32_t n, int32_t k);
+ * lora_q4_pack filled), UNSUPPORTED (T above 65535 x 16), WORKSPACE, HIP. */
+size_t lora_q4_matmul_workspace_bytes(int32_t T, int32_t n, int32_t k, int32_t group);
 int lora_q4_matmul(const void *x, int64_t ldx, const lora_q4_weight *w, int32_t T, void *y,
                    int64_t ldy, int add_inputs, void *workspace, size_t workspace_bytes,
                    void *stream);

@@ -118,8 +118,9 @@ int lora_q4_pack(const uint8_t* codes, int64_t ld_codes, const void* scales, int
                     fn);
 }
 
-size_t lora_q4_matmul_workspace_bytes(int32_t T, int32_t n, int32_t k) {
-  return T < 1 || n < 1 || k < 1 || n > 0x7fffffff - 16 || k > 0x7fffffff - 128 ? 0 : lora::q4_workspace(T, n, k);
+size_t lora_q4_matmul_workspace_bytes(int32_t T, int32_t n, int32_t k, int32_t group) {
+  if (T < 1 || check_q4(n, k, group, LORA_F16, "lora_q4_matmul_workspace_bytes")) return 0;
+  return lora::q4_workspace(T, n, k, group);
 }
 
 int lora_q4_matmul(const void* x, int64_t ldx, const lora_q4_weight* w, int32_t T, void* y, int64_t ldy,
@@ -134,8 +135,8 @@ int lora_q4_matmul(const void* x, int64_t ldx, const lora_q4_weight* w, int32_t 
   if (ldy < w->n) return fail(LORA_ERR_INVALID_ARG, "%s: ldy %lld < n %d", fn, (long long)ldy, w->n);
   if (T == 0) return ok();
   if (!x || !y) return fail(LORA_ERR_INVALID_ARG, "%s: x and y must not be NULL", fn);
-  if (T > 65535 * 128) return fail(LORA_ERR_UNSUPPORTED, "%s: T %d is too large", fn, T);
-  if (int e = check_workspace(workspace, workspace_bytes, lora::q4_workspace(T, w->n, w->k), fn)) return e;
+  if (T > 65535 * 16) return fail(LORA_ERR_UNSUPPORTED, "%s: T %d is too large", fn, T);
+  if (int e = check_workspace(workspace, workspace_bytes, lora::q4_workspace(T, w->n, w->k, w->group), fn)) return e;
   const bool x_vec = aligned(x, 16) && ldx % 8 == 0 && w->k % 8 == 0;
   const bool y_vec = aligned(y, 8) && ldy % 4 == 0 && w->n % 4 == 0;
   return hip_status(lora::launch_q4_matmul(static_cast<const uint16_t*>(x), ldx, w->packed, w->n, w->k, w->group,

@@ -55,7 +55,7 @@ hipError_t launch_q4_f16(const Q4Args& a, int sub, hipStream_t s);
 hipError_t launch_q4_bf16(const Q4Args& a, int sub, hipStream_t s);
 
 // Bytes of the splits' sums of a product (0: it does not split k).
-size_t q4_workspace(int32_t T, int32_t n, int32_t k);
+size_t q4_workspace(int32_t T, int32_t n, int32_t k, int32_t group);
 
 hipError_t launch_q4_pack(const uint8_t* codes, int64_t ld_codes, const uint16_t* scales, int64_t ld_scales,
                           const uint8_t* zeros, int64_t ld_zeros, int32_t n, int32_t k, int32_t group,

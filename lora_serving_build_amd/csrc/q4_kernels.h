@@ -141,76 +141,100 @@ __device__ __forceinline__ void q4_store(const Q4Args& a, int t, int c, f32x4 r)
 }
 
 // ---------------------------------------------------------------- product
-// For the fewest tokens: one workgroup takes MT row tiles and 16 tokens, the
-// blocks of k dealt out to its eight waves in turn; the waves' sums meet in LDS and
-// are added in wave order, so there is one launch and no workspace.  D of the
+// For few tokens or a small weight: one workgroup takes MT row tiles and 16 NT
+// tokens, the blocks of k dealt out to its eight waves in turn; the waves' sums
+// meet in LDS and are added in wave order, so there is one launch and no
+// workspace.  D of the
 // matrix core: lane l holds outputs 4 (l / 16) + 0..3 of token l % 16.
 constexpr int kWavesPerTile = 8;
 
-template <int DT, int SUB, bool ZEROS, int MT>
+template <int DT, int SUB, bool ZEROS, int MT, int NT, bool VEC>
 __global__ void __launch_bounds__(kWavesPerTile* kWave) q4_kernel(Q4Args a) {
   constexpr int W = kWavesPerTile;
-  __shared__ __align__(16) f32x4 sums[W][MT][kWave];
+  __shared__ __align__(16) f32x4 sums[W][MT * NT][kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, quad = lane >> 4;
-  const int tile0 = blockIdx.x * MT;
+  const int tile0 = blockIdx.x * MT, t0 = blockIdx.y * (16 * NT);
   const Q4Bits<DT> bits;
   // Tokens beyond T read the last row; their columns are not stored.
-  const uint16_t* xr = a.x + (int64_t)(col < a.T ? col : a.T - 1) * a.ldx + quad * 8;
+  const uint16_t* xr[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) xr[i] = a.x + (int64_t)min(t0 + i * 16 + col, a.T - 1) * a.ldx;
   // Row tiles beyond the last read the last one; their rows are not stored.
   int64_t unit0[MT];
-  f32x4 acc[MT];
+  f32x4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     unit0[m] = (int64_t)(tile0 + m < a.tiles ? tile0 + m : a.tiles - 1) * a.blocks;
-    acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
   for (int b = wave; b < a.blocks; b += W) {
     Q4Codes<SUB, MT> r;
     q4_load<DT, SUB, ZEROS, MT>(a, unit0, b, lane, &r);
-    u32x4 x[4];
-    const int h = b * 128;
-    if (a.x_vec && h + 128 <= a.k) {
+    u32x4 x[NT][4];
+    const int h = b * 128 + quad * 8;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) x[s] = *reinterpret_cast<const u32x4*>(xr + h + s * 32);
-    } else {
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) x[s] = load8_16<false>(xr + h + s * 32, a.k - quad * 8 - h - s * 32);
+      for (int s = 0; s < 4; ++s) {
+        const int at = h + s * 32;
+        x[i][s] = VEC ? *reinterpret_cast<const u32x4*>(xr[i] + (at < a.k ? at : a.k - 8)) : load8_16<false>(xr[i] + at, a.k - at);
+      }
+    if (VEC && (b + 1) * 128 > a.k) {  // inputs beyond k
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (h + s * 32 >= a.k) x[i][s] = u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int g = 0; g < SUB; ++g) {
-      f32x4 xs = {0.f, 0.f, 0.f, 0.f};
+      f32x4 xs[NT];
       if constexpr (DT == 1) {  // sums of x, in every row
         const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
-        for (int s = g * (4 / SUB); s < (g + 1) * (4 / SUB); ++s) xs = mfma16x16x32<DT>(ones, x[s], xs);
+        for (int i = 0; i < NT; ++i) {
+          xs[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = g * (4 / SUB); s < (g + 1) * (4 / SUB); ++s) xs[i] = mfma16x16x32<DT>(ones, x[i][s], xs[i]);
+        }
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const Q4Scale<DT> sc = q4_scale<DT>(r.scales[m][g], r.zeros[m][g]);
-        f32x4 part = {0.f, 0.f, 0.f, 0.f};
+        f32x4 part[NT];
 #pragma unroll
-        for (int s = g * (4 / SUB); s < (g + 1) * (4 / SUB); ++s)
-          part = mfma16x16x32<DT>(q4_numbers<DT>(r.codes[m][s], bits, sc.z_lo, sc.z_hi), x[s], part);
+        for (int i = 0; i < NT; ++i) part[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (DT == 1) part[e] = __builtin_fmaf(-sc.base[e], xs[e], part[e]);
-          acc[m][e] = __builtin_fmaf(sc.scale[e], part[e], acc[m][e]);
+        for (int s = g * (4 / SUB); s < (g + 1) * (4 / SUB); ++s) {
+          const u32x4 w = q4_numbers<DT>(r.codes[m][s], bits, sc.z_lo, sc.z_hi);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) part[i] = mfma16x16x32<DT>(w, x[i][s], part[i]);
         }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (DT == 1) part[i][e] = __builtin_fmaf(-sc.base[e], xs[i][e], part[i][e]);
+            acc[m][i][e] = __builtin_fmaf(sc.scale[e], part[i][e], acc[m][i][e]);
+          }
       }
     }
   }
 
 #pragma unroll
-  for (int m = 0; m < MT; ++m) sums[wave][m][lane] = acc[m];
-  __syncthreads();
-  for (int o = threadIdx.x; o < MT * kWave; o += W * kWave) {
-    const int l = o & (kWave - 1), m = o / kWave;
-    f32x4 r = sums[0][m][l];
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int w = 1; w < W; ++w) r += sums[w][m][l];
-    if ((l & 15) < a.T) q4_store<DT>(a, l & 15, (tile0 + m) * 16 + (l >> 4) * 4, r);
+    for (int i = 0; i < NT; ++i) sums[wave][m * NT + i][lane] = acc[m][i];
+  __syncthreads();
+  for (int o = threadIdx.x; o < MT * NT * kWave; o += W * kWave) {
+    const int l = o & (kWave - 1), mi = o / kWave, m = mi / NT, t = t0 + mi % NT * 16 + (l & 15);
+    f32x4 r = sums[0][mi][l];
+#pragma unroll
+    for (int w = 1; w < W; ++w) r += sums[w][mi][l];
+    if (t < a.T) q4_store<DT>(a, t, (tile0 + m) * 16 + (l >> 4) * 4, r);
   }
 }
 
@@ -256,7 +280,7 @@ __global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared
       const int b = min(first + chunk * CB + f / (4 * NT), last - 1), t = t0 + f / 4 % NT * 16 + col;
       const int h = b * 128 + f % 4 * 32 + quad * 8;
       const uint16_t* row = a.x + (int64_t)(t < a.T ? t : a.T - 1) * a.ldx;
-      xreg[j] = vec ? load8_16_masked(row, h, a.k, true) : load8_16<false>(row + h, a.k - h);
+      xreg[j] = vec ? *reinterpret_cast<const u32x4*>(row + (h < a.k ? h : a.k - 8)) : load8_16<false>(row + h, a.k - h);
     }
   };
   auto fetch = [&](int chunk) {
@@ -269,6 +293,10 @@ __global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared
 #pragma unroll
     for (int j = 0; j < MINE; ++j) {
       const int f = wave + j * kShareWaves;
+      // Inputs beyond k read as 0 (here and not in the fetch, which would wait
+      // for its loads there).
+      if ((first + chunk * CB + f / (4 * NT) + 1) * 128 > a.k && (first + chunk * CB + f / (4 * NT)) * 128 + f % 4 * 32 + quad * 8 >= a.k)
+        xreg[j] = u32x4{0u, 0u, 0u, 0u};
       xs[chunk & 1][f][lane] = xreg[j];
       if constexpr (DT == 1) {
         float sum = 0.f;
@@ -305,6 +333,7 @@ __global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared
       if (b >= last) break;
       const Q4Codes<SUB, MT> now = next;
       q4_load<DT, SUB, ZEROS, MT>(a, unit0, min(b + 1, last - 1), lane, &next);
+      __builtin_amdgcn_sched_barrier(0);  // the next codes leave before this block's products
 #pragma unroll
       for (int g = 0; g < SUB; ++g) {
         f32x4 part[MT][NT];
@@ -382,54 +411,74 @@ __global__ void __launch_bounds__(256) q4_add_kernel(Q4Args a, int splits) {
 // How a product is run.
 struct Q4Plan {
   bool shared;   // x through LDS, k split over workgroups
-  int mt, nt;    // row tiles of a wave, token tiles
+  int mt, nt;    // row tiles and token tiles of a workgroup (of a wave, if shared)
   int splits;
 };
 
-inline Q4Plan q4_plan(int32_t T, int32_t tiles, int32_t blocks) {
-  Q4Plan p;
-  // Row tiles of a workgroup without sharing: as many as leave one workgroup
-  // of eight waves for each CU.
-  p.shared = false;
-  p.nt = 1;
-  p.splits = 1;
-  p.mt = tiles >= 1024 ? 4 : tiles >= 512 ? 2 : 1;
-  if (T <= 16) {
-    // Without sharing, codes and x together arrive at the 9.5 TB/s or so that
-    // the L2s deliver; with it, codes at the 4.6 TB/s of memory, and a second
-    // launch with its sums costs 5 us.  Measured (bfloat16, 16 tokens): 8192
-    // outputs of 28672 inputs 38 us without, 33 with; 8192 x 8192 12.3 and
-    // 12.6; 28672 outputs of 8192 inputs 31 and 34; one token always without.
-    const double codes = (double)tiles * blocks * 1088, x = (double)(tiles / p.mt) * blocks * 256 * T;
-    p.shared = codes / 4.6e6 + 5 < (codes + x) / 9.5e6;
-    if (p.shared) p.mt = 2;
-  } else {
-    p.shared = true;
-    const int passes = (T + 127) / 128, per = ((T + passes - 1) / passes + 15) / 16;
-    p.nt = per <= 2 ? 2 : per <= 4 ? 4 : per <= 6 ? 6 : 8;
-    // Two row tiles a wave halve the LDS reads, which bound many tokens, but
-    // halve the waves too.  Measured with 64 / 128 tokens, 8192 x 8192: 25 / 55
-    // us with one, 24 / 39 with two; 4096 x 4096: 15 / 26 and 18 / 26.
-    p.mt = p.nt >= 4 && tiles >= 512 ? 2 : 1;
+// The cheapest of the kernels' forms by a cost in microseconds, fitted to
+// timings of all of them for 2 to 128 tokens, 1024 x 4096 to 28672 x 8192, one
+// sub-group of zeros a block in bfloat16 and four in binary16.
+//
+// Waves that split k: 4, and a round of 256 workgroups takes an eighth of the
+// blocks at `step` each.  The wider forms read x and the codes less often but
+// leave fewer workgroups; four sub-groups a block cost more scales and sums.
+// Waves that share x: 10 (two launches, the sums written and read), and one of
+// the splits' blocks at `step` each.
+// Measured, microseconds, first against second kind, best forms: 4096 x 4096,
+// 64 tokens 8.7 / 14.8; 5003 x 4064, 77 tokens 16 / 20; 8192 x 8192, 16 tokens
+// 12.1 / 12.6, 128 tokens 43 / 38; 8192 outputs of 28672, 16 tokens 37 / 32;
+// 28672 x 8192, 4 tokens 27 / 30, 64 tokens 85 / 60.
+inline Q4Plan q4_plan(int32_t T, int32_t tiles, int32_t blocks, int sub) {
+  struct Form {
+    int mt, nt;
+    double step, step4;  // with up to two sub-groups a block, with four
+  };
+  static const Form split_k[] = {{1, 1, 0.70, 0.80}, {2, 1, 0.85, 1.25}, {4, 1, 1.20, 2.10},
+                                 {4, 2, 2.20, 3.10}, {4, 3, 3.00, 4.00}};
+  static const Form share_x[] = {{2, 1, 0.60, 0.65}, {1, 2, 0.50, 0.65}, {2, 4, 1.55, 1.80},
+                                 {2, 6, 2.30, 2.80}, {2, 8, 3.60, 4.00}};
+  Q4Plan best{false, 1, 1, 1};
+  double least = 0;
+  for (const Form& f : split_k) {
+    const int64_t passes = (T + 16 * f.nt - 1) / (16 * f.nt), wgs = (tiles + f.mt - 1) / f.mt * passes;
+    const double cost = 4 + (double)((wgs + 255) / 256) * ((blocks + kWavesPerTile - 1) / kWavesPerTile) *
+                                (sub == 4 ? f.step4 : f.step);
+    if (least == 0 || cost < least) {
+      least = cost;
+      best = Q4Plan{false, f.mt, f.nt, 1};
+    }
   }
-  if (p.shared) {
+  for (const Form& f : share_x) {
+    // The form that just holds T; above 128 tokens the widest, in passes.
+    if (16 * f.nt < T && f.nt < 8) continue;
     // As many workgroups as CUs at most, so that none gets a second one while
     // others wait; where that leaves one split, two workgroups a CU if they fit
-    // (up to 32 tokens).  Each split has four blocks at least.  Measured with
-    // 512 row tiles, 16 tokens, k = 28672: 33 us with 8 splits (256
-    // workgroups), 42 with 10.
-    const int groups = (tiles + p.mt * kShareWaves - 1) / (p.mt * kShareWaves) * ((T + 16 * p.nt - 1) / (16 * p.nt));
-    int want = 256 / groups;
-    if (want <= 1 && p.nt <= 2) want = 512 / groups;
-    p.splits = want < blocks / 4 ? want : blocks / 4;
-    if (p.splits < 1) p.splits = 1;
+    // (up to 32 tokens).  Each split has four blocks at least.  512 row tiles, 16
+    // tokens, k = 28672: 33 us with 8 splits (256 workgroups), 42 with 10.
+    const int64_t passes = (T + 16 * f.nt - 1) / (16 * f.nt);
+    const int64_t groups = (tiles + f.mt * kShareWaves - 1) / (f.mt * kShareWaves) * passes;
+    int64_t splits = 256 / groups;
+    if (splits <= 1 && f.nt <= 2) splits = 512 / groups;
+    if (splits > blocks / 4) splits = blocks / 4;
+    if (splits < 1) splits = 1;
+    const double cost = (splits > 1 ? 10 : 6) + (double)((groups * splits + 255) / 256) *
+                                                    ((blocks + splits - 1) / splits) * (sub == 4 ? f.step4 : f.step);
+    if (cost < least) {
+      least = cost;
+      best = Q4Plan{true, f.mt, f.nt, (int)splits};
+    }
+    break;
   }
-  return p;
+  return best;
 }
 
-template <int DT, int SUB, bool ZEROS, int MT>
+template <int DT, int SUB, bool ZEROS, int MT, int NT>
 hipError_t launch_tiles(const Q4Args& a, hipStream_t s) {
-  q4_kernel<DT, SUB, ZEROS, MT><<<(a.tiles + MT - 1) / MT, kWavesPerTile * kWave, 0, s>>>(a);
+  const dim3 grid((a.tiles + MT - 1) / MT, (a.T + 16 * NT - 1) / (16 * NT));
+  if (a.x_vec)
+    q4_kernel<DT, SUB, ZEROS, MT, NT, true><<<grid, kWavesPerTile * kWave, 0, s>>>(a);
+  else
+    q4_kernel<DT, SUB, ZEROS, MT, NT, false><<<grid, kWavesPerTile * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -446,22 +495,20 @@ hipError_t launch_shared(const Q4Args& a, int splits, hipStream_t s) {
 
 template <int DT, int SUB, bool ZEROS>
 hipError_t launch_plan(const Q4Args& a, hipStream_t s) {
-  const Q4Plan p = q4_plan(a.T, a.tiles, a.blocks);
-  if (!p.shared) {
-    if (p.mt == 4) return launch_tiles<DT, SUB, ZEROS, 4>(a, s);
-    if (p.mt == 2) return launch_tiles<DT, SUB, ZEROS, 2>(a, s);
-    return launch_tiles<DT, SUB, ZEROS, 1>(a, s);
+  const Q4Plan p = q4_plan(a.T, a.tiles, a.blocks, SUB);
+  switch ((p.shared ? 64 : 0) + p.nt * 4 + p.mt - 1) {
+    case 1 * 4 + 0: return launch_tiles<DT, SUB, ZEROS, 1, 1>(a, s);
+    case 1 * 4 + 1: return launch_tiles<DT, SUB, ZEROS, 2, 1>(a, s);
+    case 1 * 4 + 3: return launch_tiles<DT, SUB, ZEROS, 4, 1>(a, s);
+    case 2 * 4 + 3: return launch_tiles<DT, SUB, ZEROS, 4, 2>(a, s);
+    case 3 * 4 + 3: return launch_tiles<DT, SUB, ZEROS, 4, 3>(a, s);
+    case 64 + 1 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 2, 1>(a, p.splits, s);
+    case 64 + 2 * 4 + 0: return launch_shared<DT, SUB, ZEROS, 1, 2>(a, p.splits, s);
+    case 64 + 4 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 2, 4>(a, p.splits, s);
+    case 64 + 6 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 2, 6>(a, p.splits, s);
+    case 64 + 8 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 2, 8>(a, p.splits, s);
   }
-  switch (p.nt * 4 + p.mt) {
-    case 1 * 4 + 2: return launch_shared<DT, SUB, ZEROS, 2, 1>(a, p.splits, s);
-    case 2 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 2>(a, p.splits, s);
-    case 4 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 4>(a, p.splits, s);
-    case 4 * 4 + 2: return launch_shared<DT, SUB, ZEROS, 2, 4>(a, p.splits, s);
-    case 6 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 6>(a, p.splits, s);
-    case 6 * 4 + 2: return launch_shared<DT, SUB, ZEROS, 2, 6>(a, p.splits, s);
-    case 8 * 4 + 1: return launch_shared<DT, SUB, ZEROS, 1, 8>(a, p.splits, s);
-    default: return launch_shared<DT, SUB, ZEROS, 2, 8>(a, p.splits, s);
-  }
+  return hipErrorInvalidValue;  // not reached
 }
 
 template <int DT>

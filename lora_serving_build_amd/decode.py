@@ -97,7 +97,7 @@ def _declare(L) -> None:
     L.lora_q4_packed_bytes.argtypes = [i32, i32, i32, ci]
     L.lora_q4_packed_bytes.restype = sz
     L.lora_q4_pack.argtypes = [p, i64, p, i64, p, i64, i32, i32, i32, ci, p, sz, p, p]
-    L.lora_q4_matmul_workspace_bytes.argtypes = [i32, i32, i32]
+    L.lora_q4_matmul_workspace_bytes.argtypes = [i32, i32, i32, i32]
     L.lora_q4_matmul_workspace_bytes.restype = sz
     L.lora_q4_matmul.argtypes = [p, i64, p, i32, p, i64, ci, p, sz, p]
     L.lora_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
@@ -224,8 +224,8 @@ def lora_q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor 
     return w
 
 
-def lora_q4_matmul_workspace_bytes(T: int, n: int, k: int) -> int:
-    return int(_base.lib().lora_q4_matmul_workspace_bytes(int(T), int(n), int(k)))
+def lora_q4_matmul_workspace_bytes(T: int, n: int, k: int, group: int) -> int:
+    return int(_base.lib().lora_q4_matmul_workspace_bytes(int(T), int(n), int(k), int(group)))
 
 
 def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bool = False,
@@ -246,7 +246,7 @@ def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bo
     at = _gpu(w.packed, x, y, workspace)
     stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(at, stream, L.lora_q4_matmul_workspace_bytes(T, n, k), workspace)
+    ws, ws_bytes = _workspace(at, stream, L.lora_q4_matmul_workspace_bytes(T, n, k, w.group), workspace)
     _run(L.lora_q4_matmul(x.data_ptr(), ldx, w._ref, T, y.data_ptr(), ldy, 1 if add_inputs else 0, ws, ws_bytes, stream))
     return y
 

@@ -81,14 +81,15 @@ def test_q4_matmul_refusals():
     _expect(call(ldx=127), BAD, "ldx")
     _expect(call(ldy=15), BAD, "ldy")
     _expect(call(x=None), BAD, "must not be NULL")
-    _expect(call(T=65535 * 128 + 1), UNS, "too large")
-    need = lsb.lora_q4_matmul_workspace_bytes(40, 16, 4096)
-    assert need > 0 and lsb.lora_q4_matmul_workspace_bytes(1, 16, 4096) == 0
-    _expect(call(T=40, k=4096, ws=FAKE, ws_bytes=need - 1), WS, "workspace")
-    _expect(call(T=40, k=4096), WS, "workspace")
-    _expect(call(T=40, k=4096, ws=FAKE + 8, ws_bytes=need), WS, "aligned")
+    _expect(call(T=65535 * 16 + 1), UNS, "too large")
+    size = dict(T=64, n=28672, k=8192, ldx=8192, ldy=28672)
+    need = lsb.lora_q4_matmul_workspace_bytes(64, 28672, 8192, 128)
+    assert need > 0 and lsb.lora_q4_matmul_workspace_bytes(1, 16, 4096, 128) == 0
+    _expect(call(ws=FAKE, ws_bytes=need - 1, **size), WS, "workspace")
+    _expect(call(**size), WS, "workspace")
+    _expect(call(ws=FAKE + 8, ws_bytes=need, **size), WS, "aligned")
     assert call(T=0) == lsb.LORA_OK
-    for sizes in ((0, 16, 128), (4, 0, 128), (4, 16, 0)):
+    for sizes in ((0, 16, 128, 32), (4, 0, 128, 32), (4, 16, 0, 32), (4, 16, 128, 40)):
         assert lsb.lora_q4_matmul_workspace_bytes(*sizes) == 0
 
 

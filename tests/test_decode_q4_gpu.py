@@ -72,6 +72,15 @@ CASES = [
     (260, 33, 1280, 128, True, "bf16"),
     (4, 2048, 8192, 128, True, "bf16"),
     (16, 512, 16384, 64, False, "f16"),
+    (16, 8200, 4000, 64, False, "bf16"),
+    (40, 8192, 1024, 32, True, "f16"),
+    (100, 4099, 1032, 128, True, "bf16"),
+    (30, 14336, 2048, 128, False, "f16"),
+    (60, 16384, 2048, 64, True, "bf16"),
+    (90, 16390, 2056, 32, False, "f16"),
+    (128, 16384, 2048, 128, True, "bf16"),
+    (200, 8192, 4096, 128, True, "f16"),
+    (11, 4096, 20480, 128, False, "bf16"),
 ]
 
 
