@@ -113,16 +113,16 @@ __device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
   const int group = a.heads / a.kv_heads;
   const int part = (blockIdx.x & 7) * (kParts / 8) + (blockIdx.x >> 3);
   auto lines_of = [&](const Seq& s) { return row_tiles(s.n, group, ROWS) * a.kv_heads; };
+  // Sequence base + lane, empty beyond the last; the first 64 are read once.
+  auto read = [&](int base) { return base + lane < a.B ? sequence(a, base + lane) : Seq{0, 0, 0, 0}; };
+  const Seq head = read(0);
+  auto seq_at = [&](int base) { return base == 0 ? head : read(base); };
   uint32_t lines = 0, tiles = 0;
   for (int base = 0; base < a.B; base += kWave) {
-    int l = 0, t = 0;
-    if (base + lane < a.B) {
-      const Seq s = sequence(a, base + lane);
-      l = lines_of(s);
-      t = l * key_tiles(s.len, KEYS);
-    }
+    const Seq s = seq_at(base);
+    const int l = lines_of(s);
     lines += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(l), kWave - 1);
-    tiles += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(t), kWave - 1);
+    tiles += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(l * key_tiles(s.len, KEYS)), kWave - 1);
   }
   // With fewer tiles than parts every tile is a part.
   const int cost = tiles <= (uint32_t)kParts ? 0 : COST;
@@ -139,11 +139,8 @@ __device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
   }
   int before = 0, b = -1, start = 0;
   for (int base = 0; base < a.B; base += kWave) {
-    int mine = 0;
-    if (base + lane < a.B) {
-      const Seq s = sequence(a, base + lane);
-      mine = lines_of(s) * (cost + key_tiles(s.len, KEYS));
-    }
+    const Seq s = seq_at(base);
+    const int mine = lines_of(s) * (cost + key_tiles(s.len, KEYS));
     const int end = before + wave_inclusive_sum(mine);
     if (part == 0 && threadIdx.x < kWave && base + lane < a.B) space(a).first[base + lane] = end - mine;
     const uint64_t m = __ballot(p->at < end && p->at >= end - mine);
@@ -251,9 +248,16 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Place& it,
   }
 }
 
+// First word of a row's mask (all ones without one).
+__device__ __forceinline__ uint64_t first_mask_word(const AttnArgs& a, const Place& it, int node) {
+  if (!a.mask) return ~0ull;
+  return a.mask_words > 0 ? a.mask[(int64_t)(it.s.q0 + node) * a.ld_mask] : 0ull;
+}
+
 // Which of the positions key0 .. key0 + 31 row `node` sees, one bit each;
-// `there`: the positions that exist.
-__device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const Place& it, int node, int key0, uint32_t there) {
+// `there`: the positions that exist; `word`: the first of the row's mask.
+__device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const Place& it, int node, uint64_t word, int key0,
+                                              uint32_t there) {
   const int j0 = key0 - it.s.ctx;  // the node at position key0; at least -31 where it matters
   if (j0 <= -32) return there;
   uint32_t bits;
@@ -262,11 +266,10 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const Place& it
     // behind the last word.
     const uint64_t* row = a.mask + (int64_t)(it.s.q0 + node) * a.ld_mask;
     const int w = j0 >> 6, sh = j0 & 63, last = a.mask_words - 1;
-    uint64_t lo = w < 0 ? ~0ull : 0ull, hi = 0ull;
-    if (last >= 0) {
-      const uint64_t x = row[min(max(w, 0), last)], y = row[min(w + 1, last)];
-      if (w >= 0 && w <= last) lo = x;
-      if (w < last) hi = y;
+    uint64_t lo = w < 0 ? ~0ull : w == 0 ? word : 0ull, hi = w < 0 ? word : 0ull;
+    if (w >= 0 && last > 0) {
+      if (w > 0 && w <= last) lo = row[w];
+      if (w < last) hi = row[w + 1];
     }
     bits = (uint32_t)((lo >> sh) | (sh ? hi << (64 - sh) : 0ull));
   } else {
@@ -286,57 +289,70 @@ __device__ __forceinline__ void mask_scores(uint32_t seen, int quad, f32x4 (&s)[
       if (!((seen >> (t * 16 + quad * 4 + e)) & 1)) s[t][e] = -INFINITY;
 }
 
-// One step of the running softmax of a row tile: raw scores in, weights out
-// (and as the 16-bit operand of the value product).  c = |scale| log2 e.  The
-// reference score m follows the maximum only when that has grown by 2^6 in
+// One step of the running softmax of RT row tiles: raw scores in, weights out
+// (and as the 16-bit operands of the value product).  c = |scale| log2 e.  The
+// reference scores m follow the maxima only when one has grown by 2^6 in
 // weight: until then the weights are at most 64, which loses nothing in fp32
-// sums and saves the scaling of l and o.
-template <int DT, int N>
-__device__ __forceinline__ u32x4 weigh(f32x4 (&s)[2], float c, float& m, float& l, f32x4 (&o)[N]) {
-  float top = fmaxf(fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[0].z, s[0].w)),
-                    fmaxf(fmaxf(s[1].x, s[1].y), fmaxf(s[1].z, s[1].w)));
-  top = max_over_lane_groups(top);
-  if (__any((top - m) * c > 6.f)) {
-    const float now = fmaxf(top, m);
-    const float shrink = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - now) * c);
-    l *= shrink;
+// sums and saves the scaling of l and o.  One branch for all row tiles: their
+// chains of dependent operations run side by side.
+template <int DT, int RT, int N>
+__device__ __forceinline__ void weigh(f32x4 (&s)[RT][2], float c, float (&m)[RT], float (&l)[RT], f32x4 (&o)[RT][N],
+                                      u32x4 (&w)[RT]) {
+  float top[RT];
+  bool grown = false;
 #pragma unroll
-    for (int d = 0; d < N; ++d) o[d] *= shrink;
-    m = now;
+  for (int r = 0; r < RT; ++r) {
+    top[r] = fmaxf(fmaxf(fmaxf(s[r][0].x, s[r][0].y), fmaxf(s[r][0].z, s[r][0].w)),
+                   fmaxf(fmaxf(s[r][1].x, s[r][1].y), fmaxf(s[r][1].z, s[r][1].w)));
+    top[r] = max_over_lane_groups(top[r]);
+    grown |= (top[r] - m[r]) * c > 6.f;
   }
-  const float base = m == -INFINITY ? 0.f : -m * c;
+  if (__any(grown)) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+    for (int r = 0; r < RT; ++r) {
+      const float now = fmaxf(top[r], m[r]);
+      const float shrink = m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[r] - now) * c);
+      l[r] *= shrink;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s[t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][e], c, base));
-      l += s[t][e];
+      for (int d = 0; d < N; ++d) o[r][d] *= shrink;
+      m[r] = now;
     }
-  return u32x4{cvt_pack2<DT>(s[0].x, s[0].y), cvt_pack2<DT>(s[0].z, s[0].w), cvt_pack2<DT>(s[1].x, s[1].y),
-               cvt_pack2<DT>(s[1].z, s[1].w)};
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const float base = m[r] == -INFINITY ? 0.f : -m[r] * c;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[r][t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t][e], c, base));
+        l[r] += s[r][t][e];
+      }
+    w[r] = u32x4{cvt_pack2<DT>(s[r][0].x, s[r][0].y), cvt_pack2<DT>(s[r][0].z, s[r][0].w),
+                 cvt_pack2<DT>(s[r][1].x, s[r][1].y), cvt_pack2<DT>(s[r][1].z, s[r][1].w)};
+  }
 }
 
 // Adds the value row p (position i of the step), which is not finite
 // throughout and was kept out of the products, to the rows that see it.
 template <int DT, int N>
-__device__ __forceinline__ void add_odd_value(const uint16_t* p, int i, int dim, int col, int quad, const f32x4 (&s)[2],
+__device__ __forceinline__ void add_odd_value(const uint16_t* p, int i, int dim, int col, int quad, u32x4 w,
                                               f32x4 (&o)[N]) {
-  const int src = (i % 16 / 4) * 16 + col;
-  float weight = 0.f;
+  // Weight of position 16 t + 4 q + e: lane (q, col), half e % 2 of dword 2 t + e / 2.
+  uint32_t two = 0;
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = __shfl(s[t][e], src);
-      if (i / 16 == t && i % 4 == e) weight = x;
-    }
+  for (int x = 0; x < 4; ++x)
+    if (i / 16 * 2 + i % 4 / 2 == x) two = w[x];
+  two = __shfl(two, (i % 16 / 4) * 16 + col);
+  const float weight = to_f32<DT>(i % 2 ? two >> 16 : two & 0xffffu);
 #pragma unroll
   for (int d = 0; d < N; ++d) {
+    __builtin_amdgcn_sched_barrier(0);  // one load at a time: registers count, time does not
     const int c = d * 16 + quad * 4;
-    const u32x2 two = *reinterpret_cast<const u32x2*>(p + (c < dim ? c : dim - 4));
+    const u32x2 four = *reinterpret_cast<const u32x2*>(p + (c < dim ? c : dim - 4));
     float x[4];
-    unpack2<DT>(two.x, &x[0], &x[1]);
-    unpack2<DT>(two.y, &x[2], &x[3]);
+    unpack2<DT>(four.x, &x[0], &x[1]);
+    unpack2<DT>(four.y, &x[2], &x[3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (weight != 0.f) o[d][e] += weight * x[e];
@@ -397,16 +413,17 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
 
     const int my_row = min(row0 + col, rows - 1);  // rows beyond the last read the last one
     const int node = my_row / group;
+    const uint64_t word = first_mask_word(a, it, node);
     u32x4 q[KS];
     load_queries<DP>(a, it, node, it.h * group + my_row % group, quad, q);
     const uint16_t* kbase = a.k + it.h * a.kv_head;
     const uint16_t* vbase = a.v + it.h * a.kv_head;
     const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
 
-    f32x4 o[OT];
-    float m = -INFINITY, l = 0.f;
+    f32x4 o[1][OT];
+    float m[1] = {-INFINITY}, l[1] = {0.f};
 #pragma unroll
-    for (int d = 0; d < OT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < OT; ++d) o[0][d] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // Page of position key0 + lane % 32 (of the last one, where that is beyond
     // the end), and the cache row that follows from it.
@@ -445,12 +462,12 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
       const int64_t here = at < 0 ? 0 : at;
 
       // Scores: lane holds positions key0 + 16 t + 4 quad + e of row col.
-      f32x4 sc[2];
+      f32x4 sc[1][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        sc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) sc[t] = mfma16x16x32<DT>(k[t][s], q[s], sc[t]);
+        for (int s = 0; s < KS; ++s) sc[0][t] = mfma16x16x32<DT>(k[t][s], q[s], sc[0][t]);
       }
 
       // Values that are not finite are kept out of the products with weight 0:
@@ -483,8 +500,9 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
       if (next < end) load(at < 0 ? 0 : at);
       page = page_of(next + TILE);
 
-      if (drafted || there != 0xffffffffu) mask_scores(seen_bits(a, it, node, key0, there), quad, sc);
-      const u32x4 w = weigh<DT, OT>(sc, c, m, l, o);
+      if (drafted || there != 0xffffffffu) mask_scores(seen_bits(a, it, node, word, key0, there), quad, sc[0]);
+      u32x4 w[1];
+      weigh<DT, 1, OT>(sc, c, m, l, o, w);
 
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -492,28 +510,28 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
         // Elements 0..3: positions 4 quad + 0..3 of the first 16, 4..7 of the second.
         const uint16_t* p = stage + (quad * 4 + (col >> 2)) * PITCH + d * 16 + (col & 3) * 4;
         const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * PITCH);
-        o[d] = mfma16x16x32<DT>(u32x4{lo.x, lo.y, hi.x, hi.y}, w, o[d]);
+        o[0][d] = mfma16x16x32<DT>(u32x4{lo.x, lo.y, hi.x, hi.y}, w[0], o[0][d]);
       }
       __builtin_amdgcn_wave_barrier();
 
       while (odd) {
         const int i = __ffs(odd) - 1;
         odd &= odd - 1;
-        add_odd_value<DT, OT>(vbase + __shfl(here, i), i, a.dim, col, quad, sc, o);
+        add_odd_value<DT, OT>(vbase + __shfl(here, i), i, a.dim, col, quad, w[0], o[0]);
       }
     }
 
     // Join the waves.
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
+    l[0] += __shfl_xor(l[0], 16);
+    l[0] += __shfl_xor(l[0], 32);
     if (quad == 0) {
-      row_max[wave][col] = m * c;
-      row_sum[wave][col] = l;
+      row_max[wave][col] = m[0] * c;
+      row_sum[wave][col] = l[0];
     }
     __syncthreads();  // every wave is done with its values
 #pragma unroll
     for (int d = 0; d < OT; ++d)
-      *reinterpret_cast<f32x4*>(join + (wave * ROWS + col) * JP + d * 16 + quad * 4) = o[d];
+      *reinterpret_cast<f32x4*>(join + (wave * ROWS + col) * JP + d * 16 + quad * 4) = o[0][d];
     __syncthreads();
     float* slot = nullptr;
     if (to - from < it.tiles)
@@ -593,10 +611,12 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
 
     u32x4 q[RT][KS];
     int node[RT];
+    uint64_t word[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const int row = min(row0 + r * 16 + col, rows - 1);
       node[r] = row / group;
+      word[r] = first_mask_word(a, it, node[r]);
       load_queries<DP>(a, it, node[r], it.h * group + row % group, quad, q[r]);
     }
     const uint16_t* vhead = a.v + it.h * a.kv_head;
@@ -614,7 +634,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       for (int d = 0; d < OT; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    u32x4 reg[PASS];  // a tile's keys during its first half, its values after that
+    u32x4 reg[PASS];  // the next tile's keys during the first half of this one, its values after that
     // Page of a position of tile n (each wave looks up all of them), and the
     // cache row that follows from it.  The two are apart so that the page is on
     // its way during a whole tile.
@@ -644,14 +664,21 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
     auto stash_values = [&](int n, uint64_t there) {
       const bool plain = begin + (n + 1) * KEYS <= it.s.ctx && (KEYS == 64 ? !~there : (uint32_t)there == ~0u);
       if (!plain) {
+        bool bad = false;
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
-          const int r = prow + i * RPP, first = lane / CPR * CPR;
-          const bool absent = !((there >> r) & 1);
-          const uint64_t lanes = __ballot(not_finite<DT>(reg[i]) && !absent);
-          const bool odd = lanes && ((lanes >> first) & ((1ull << CPR) - 1ull));
-          if (odd && lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
-          if (absent || odd) reg[i] = u32x4{0u, 0u, 0u, 0u};
+          if (!((there >> (prow + i * RPP)) & 1)) reg[i] = u32x4{0u, 0u, 0u, 0u};
+          bad |= not_finite<DT>(reg[i]);
+        }
+        if (__builtin_expect(__any(bad), 0)) {
+#pragma unroll
+          for (int i = 0; i < PASS; ++i) {
+            const int r = prow + i * RPP, first = lane / CPR * CPR;
+            const uint64_t lanes = __ballot(not_finite<DT>(reg[i]));
+            const bool odd = lanes && ((lanes >> first) & ((1ull << CPR) - 1ull));
+            if (odd && lane == first) atomicOr(&odd_rows[n & 1][r / 32], 1u << (r % 32));
+            if (odd) reg[i] = u32x4{0u, 0u, 0u, 0u};
+          }
         }
       }
       if (piece < a.dim) {
@@ -716,6 +743,10 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < RT; ++r) sc[r][t] = mfma16x16x32<DT>(kf[t][s], q[r][s], sc[r][t]);
+        if (__builtin_expect(key0 + 32 > it.s.ctx || there != 0xffffffffu, 0)) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) mask_scores(seen_bits(a, it, node[r], word[r], key0, there), quad, sc[r]);
+        }
         u32x4 vf[OT];
 #pragma unroll
         for (int d = 0; d < OT; ++d) {
@@ -724,24 +755,19 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
           vf[d] = u32x4{lo.x, lo.y, hi.x, hi.y};
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (key0 + 32 > it.s.ctx || there != 0xffffffffu) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r) mask_scores(seen_bits(a, it, node[r], key0, there), quad, sc[r]);
-        }
         u32x4 w[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) w[r] = weigh<DT, OT>(sc[r], c, m[r], l[r], o[r]);
+        weigh<DT, RT, OT>(sc, c, m, l, o, w);
 #pragma unroll
         for (int d = 0; d < OT; ++d)
 #pragma unroll
           for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf[d], w[r], o[r][d]);
         uint32_t odd = odd_rows[n & 1][half];
-        while (odd) {
+        while (__builtin_expect(odd != 0, 0)) {
           const int i = __ffs(odd) - 1;
           odd &= odd - 1;
           const uint16_t* p = vhead + where[n & 3][half * 32 + i];
 #pragma unroll
-          for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, sc[r], o[r]);
+          for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, w[r], o[r]);
         }
       }
       // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
@@ -791,20 +817,18 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
 }
 
 // ---------------------------------------------------------------- join of pieces
-// A row (token, head) is joined by SHARE waves, wave w of them taking pieces w,
-// w + SHARE, ...; 64 lanes hold the DP columns.  SHARE = 8 (a block a row) while
-// the rows are few and their pieces many, else 1.  A wave reads a batch of pieces
-// at once, with a running maximum and sum over the batches, so that few memory
-// latencies follow the look-ups (48 nodes x 16 sequences x 64 heads: 28 us piece
-// by piece, 24 in batches).
-template <int DT, int DP, int ROWS, int KEYS, int SHARE>
-__global__ void __launch_bounds__((SHARE == 1 ? kWaves : SHARE) * kWave) join_kernel(AttnArgs a) {
+// For few rows, whose lines are cut into many pieces: a block of eight waves
+// joins one row (token, head), wave w taking pieces w, w + 8, ...; 64 lanes hold
+// the DP columns.  A wave reads a batch of pieces at once, with a running maximum
+// and sum over the batches, so that few memory latencies follow the look-ups.
+constexpr int kJoinWaves = 8;
+
+template <int DT, int DP, int ROWS, int KEYS>
+__global__ void __launch_bounds__(kJoinWaves* kWave) join_kernel(AttnArgs a) {
   constexpr int PER = DP / kWave;
   const Space sp = space(a);
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t out_row = SHARE == 1 ? (int64_t)blockIdx.x * kWaves + wave : (int64_t)blockIdx.x;
-  if (out_row >= (int64_t)a.T * a.heads) return;
-  const int t = (int)(out_row / a.heads), head = (int)(out_row % a.heads);
+  const int t = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
   const int group = a.heads / a.kv_heads;
   // The sequence of token t.
   int b = -1;
@@ -824,15 +848,15 @@ __global__ void __launch_bounds__((SHARE == 1 ? kWaves : SHARE) * kWave) join_ke
   auto piece = [&](int i) {
     return sp.slots + (int64_t)slot_of(part0 + i, part_cost, tiles0) * slot_floats<DP, ROWS>();
   };
-  constexpr int BATCH = SHARE == 1 ? 4 : 12;
+  constexpr int BATCH = 12;
   float top = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int i0 = SHARE == 1 ? 0 : wave; i0 < splits; i0 += SHARE * BATCH) {
+  for (int i0 = wave; i0 < splits; i0 += kJoinWaves * BATCH) {
     float m[BATCH], l[BATCH], v[BATCH][PER];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {  // pieces beyond the last: the last one, with no weight
-      const float* p = piece(min(i0 + i * SHARE, splits - 1));
+      const float* p = piece(min(i0 + i * kJoinWaves, splits - 1));
       m[i] = p[ROWS * DP + in_tile];
       l[i] = p[ROWS * DP + ROWS + in_tile];
       if constexpr (PER == 1) {
@@ -855,15 +879,15 @@ __global__ void __launch_bounds__((SHARE == 1 ? kWaves : SHARE) * kWave) join_ke
     top = now;
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (i0 + i * SHARE >= splits) continue;
+      if (i0 + i * kJoinWaves >= splits) continue;
       const float f = __builtin_amdgcn_exp2f(m[i] - base);
       sum += f * l[i];
 #pragma unroll
       for (int e = 0; e < PER; ++e) acc[e] += f * v[i][e];
     }
   }
-  if constexpr (SHARE > 1) {
-    __shared__ float part[SHARE][DP + 2];
+  {
+    __shared__ float part[kJoinWaves][DP + 2];
 #pragma unroll
     for (int e = 0; e < PER; ++e) part[wave][lane * PER + e] = acc[e];
     if (lane == 0) {
@@ -873,13 +897,13 @@ __global__ void __launch_bounds__((SHARE == 1 ? kWaves : SHARE) * kWave) join_ke
     __syncthreads();
     if (wave != 0) return;
 #pragma unroll
-    for (int w = 1; w < SHARE; ++w) top = fmaxf(top, part[w][DP + 1]);
+    for (int w = 1; w < kJoinWaves; ++w) top = fmaxf(top, part[w][DP + 1]);
     const float base = top == -INFINITY ? 0.f : top;
     sum = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int w = 0; w < SHARE; ++w) {
+    for (int w = 0; w < kJoinWaves; ++w) {
       const float f = __builtin_amdgcn_exp2f(part[w][DP + 1] - base);
       sum += f * part[w][DP];
 #pragma unroll
@@ -895,6 +919,101 @@ __global__ void __launch_bounds__((SHARE == 1 ? kWaves : SHARE) * kWave) join_ke
   if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads + head] = log_sum(base, sum);
 }
 
+// For many rows: blocks take lines, kSlice rows of each (blockIdx.y), so that one
+// look-up serves them and a line that was not cut costs one short block; a wave
+// has four rows' pieces on their way at once (48 nodes x 16 sequences x 64 heads:
+// 24 us with a wave for each row, 16 of them where no line is cut).
+constexpr int kSlice = 32;
+
+template <int DT, int DP, int ROWS, int KEYS>
+__global__ void __launch_bounds__(kWaves* kWave) join_lines_kernel(AttnArgs a) {
+  constexpr int PER = DP / kWave, AT_ONCE = 4, BATCH = DP == 256 ? 2 : 3;
+  constexpr int SLICE = ROWS < kSlice ? ROWS : kSlice;
+  typedef float Vec __attribute__((ext_vector_type(PER == 1 ? 2 : PER)));
+  Place it;
+  if (!find_line<ROWS, KEYS>(a, &it)) return;
+  const Space sp = space(a);
+  const int part_cost = sp.part[0], cost = sp.part[1];
+  const int tiles0 = sp.first[it.b] + (it.h * it.rts + it.rt) * (cost + it.tiles) + cost;
+  const int part0 = tiles0 / part_cost, splits = min((tiles0 + it.tiles - 1) / part_cost, kParts - 1) - part0 + 1;
+  if (splits < 2) return;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int group = a.heads / a.kv_heads, rows = it.s.n * group, row0 = it.rt * ROWS;
+  auto piece = [&](int i) {
+    return sp.slots + (int64_t)slot_of(part0 + i, part_cost, tiles0) * slot_floats<DP, ROWS>();
+  };
+  for (int r0 = blockIdx.y * SLICE + wave * AT_ONCE; r0 < (blockIdx.y + 1) * SLICE && row0 + r0 < rows;
+       r0 += kWaves * AT_ONCE) {
+    float top[AT_ONCE], sum[AT_ONCE], acc[AT_ONCE][PER];
+#pragma unroll
+    for (int r = 0; r < AT_ONCE; ++r) {
+      top[r] = -INFINITY;
+      sum[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[r][e] = 0.f;
+    }
+    for (int i0 = 0; i0 < splits; i0 += BATCH) {
+      float m[BATCH][AT_ONCE], l[BATCH][AT_ONCE], v[BATCH][AT_ONCE][PER];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {  // pieces beyond the last: the last one, with no weight
+        const float* p = piece(min(i0 + i, splits - 1));
+#pragma unroll
+        for (int r = 0; r < AT_ONCE; ++r) {
+          m[i][r] = p[ROWS * DP + r0 + r];
+          l[i][r] = p[ROWS * DP + ROWS + r0 + r];
+          if constexpr (PER == 1) {
+            v[i][r][0] = p[(r0 + r) * DP + lane];
+          } else {
+            const Vec x = *reinterpret_cast<const Vec*>(p + (r0 + r) * DP + lane * PER);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v[i][r][e] = x[e];
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < AT_ONCE; ++r) {
+        float now = top[r];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) now = fmaxf(now, m[i][r]);
+        const float base = now == -INFINITY ? 0.f : now;
+        const float shrink = __builtin_amdgcn_exp2f(top[r] - base);
+        sum[r] *= shrink;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[r][e] *= shrink;
+        top[r] = now;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          if (i0 + i >= splits) continue;
+          const float f = __builtin_amdgcn_exp2f(m[i][r] - base);
+          sum[r] += f * l[i][r];
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[r][e] += f * v[i][r][e];
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < AT_ONCE; ++r) {
+      const int row = row0 + r0 + r;
+      if (row >= rows) continue;
+      const int t = it.s.q0 + row / group, head = it.h * group + row % group;
+      const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+      uint16_t* out = a.out + t * a.out_token + head * a.out_head;
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (lane * PER + e < a.dim) out[lane * PER + e] = (uint16_t)from_f32<DT>(acc[r][e] * inv);
+      if (a.lse && lane == 0)
+        a.lse[(int64_t)t * a.heads + head] = log_sum(top[r] == -INFINITY ? 0.f : top[r], sum[r]);
+    }
+  }
+}
+
+// Most lines a call can have: every sequence has at most one row tile that is
+// not full.
+int64_t line_bound(const AttnArgs& a, int tile_rows) {
+  const int64_t rows = (int64_t)a.T * (a.heads / a.kv_heads);
+  return (rows / tile_rows + (a.B < rows ? a.B : rows)) * a.kv_heads;
+}
+
 // ROWS = 16: the kernel for few rows; 64, 128: the one for many.
 template <int DT, int DP, int ROWS>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
@@ -906,10 +1025,12 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t out_rows = (int64_t)a.T * a.heads;
-  if (out_rows <= kCus * 8)
-    join_kernel<DT, DP, ROWS, KEYS, 8><<<(unsigned)out_rows, 8 * kWave, 0, s>>>(a);
-  else
-    join_kernel<DT, DP, ROWS, KEYS, 1><<<(unsigned)((out_rows + kWaves - 1) / kWaves), kWaves * kWave, 0, s>>>(a);
+  if (out_rows <= kCus * 8) {
+    join_kernel<DT, DP, ROWS, KEYS><<<(unsigned)out_rows, kJoinWaves * kWave, 0, s>>>(a);
+  } else {
+    const dim3 grid((unsigned)line_bound(a, ROWS), (ROWS + kSlice - 1) / kSlice);
+    join_lines_kernel<DT, DP, ROWS, KEYS><<<grid, kWaves * kWave, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -920,11 +1041,8 @@ bool short_lines(const AttnArgs& a) { return (int64_t)a.max_pages * a.page_size 
 
 template <int DT, int DP>
 hipError_t launch_short(const AttnArgs& a, hipStream_t s) {
-  const int64_t rows = (int64_t)a.T * (a.heads / a.kv_heads);
-  // Every sequence has at most one row tile that is not full.
-  const int64_t lines = (rows / 16 + (a.B < rows ? a.B : rows)) * a.kv_heads;
   constexpr int W = DP == 256 ? 4 : 8;  // what the registers allow
-  attention_kernel<DT, DP, W, true><<<(unsigned)lines, W * kWave, 0, s>>>(a);
+  attention_kernel<DT, DP, W, true><<<(unsigned)line_bound(a, 16), W * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -81,6 +81,13 @@ CASES = [
     (128, 16384, 2048, 128, True, "bf16"),
     (200, 8192, 4096, 128, True, "f16"),
     (11, 4096, 20480, 128, False, "bf16"),
+    # the forms that split k over workgroups, by tokens
+    (1, 509, 10744, 32, True, "f16"),
+    (26, 512, 10752, 32, False, "bf16"),
+    (58, 505, 16888, 32, True, "bf16"),
+    (90, 512, 21990, 128, False, "f16"),
+    (122, 22012, 512, 32, True, "bf16"),
+    (257, 512, 10745, 32, False, "f16"),
 ]
 
 
