@@ -120,7 +120,8 @@ typedef struct lora_kv_layer {
  * needs no initialisation.  Calls that run concurrently must not share it.
  * Same inputs give the same bits.
  * Errors: INVALID_ARG (NULL, sizes, strides, alignment, dtype), UNSUPPORTED
- * (dim, or more than 2^31 - 1 positions in a row of the table), WORKSPACE, HIP. */
+ * (dim; a table row of more than 2^31 - 256 positions; 2^31 or more units of 16
+ * rows, a key head and 32 positions of the table), WORKSPACE, HIP. */
 size_t lora_tree_attention_workspace_bytes(int32_t B, int32_t T, int32_t heads, int32_t kv_heads,
                                            int32_t dim);
 int lora_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,

@@ -282,6 +282,12 @@ int lora_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   if (!aligned(q, 16) || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(out, 8))
     return fail(LORA_ERR_INVALID_ARG, "%s: q, k and v must be 16-byte aligned, out 8-byte", fn);
   if ((int64_t)b.T * heads > 0x3fffffff) return fail(LORA_ERR_UNSUPPORTED, "%s: T %d x heads %d is too large", fn, b.T, heads);
+  // The kernels count (row tile, key head, tile of positions) units in 32 bits.
+  const int64_t rows = (int64_t)b.T * (heads / kv_heads), tiles = rows / 16 + (b.B < rows ? b.B : rows);
+  const int64_t units = (int64_t)b.max_pages * c.page_size / 32 + 8;
+  if (tiles * kv_heads > 0x7fffffff / units)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: %lld row tiles of up to %lld positions are too many", fn,
+                (long long)(tiles * kv_heads), (long long)b.max_pages * c.page_size);
   if (b.B == 0 || b.T == 0) return ok();
   if (!q || !out || !b.start || !b.ctx_len || (b.max_pages > 0 && !b.table) || (c.num_pages > 0 && (!c.k || !c.v)))
     return fail(LORA_ERR_INVALID_ARG, "%s: q, out, start, ctx_len, table, k and v must not be NULL", fn);

@@ -230,21 +230,29 @@ __global__ void __launch_bounds__(kScanThreads) fork_plan_kernel(PageView c, con
   __shared__ int scratch[kScanThreads / kWave + 1];
   __shared__ int32_t ids[kMaxPageEntries];
   __shared__ int32_t who[kMaxPageEntries];  // entry of the rank-th page
-  const int tid = threadIdx.x;
-  for (int i = tid; i < n; i += kScanThreads) ids[i] = dst[i];
+  __shared__ uint8_t needs[kMaxPageEntries];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  for (int i = tid; i < n; i += kScanThreads) {
+    const int32_t d = dst[i], s = src[i];
+    ids[i] = d;
+    const bool good = fork_entry_good(c, s, d);
+    needs[i] = !good ? 2 : c.seq_len[s] % c.page_size != 0;
+  }
+  __syncthreads();
+  // A wave looks for each entry's destination among the earlier ones.
+  for (int i = wave; i < n; i += kScanThreads / kWave) {
+    bool same = false;
+    for (int j = lane; j < i; j += kWave) same |= ids[j] == ids[i];
+    if (__any(same) && lane == 0) needs[i] = 2;
+  }
   __syncthreads();
   int total = 0;
   for (int base = 0; base < n; base += kScanThreads) {
     const int i = base + tid;
-    int need = 0;
-    if (i < n) {
-      bool good = fork_entry_good(c, src[i], ids[i]);
-      for (int j = 0; j < i; ++j) good &= ids[j] != ids[i];
-      need = good && c.seq_len[src[i]] % c.page_size != 0;
-      if (!need) {
-        ws.fresh[i] = good ? kNone : kBadEntry;
-        if (status) status[i] = good ? kOk : kBad;
-      }
+    const int state = i < n ? needs[i] : 0, need = state == 1;
+    if (i < n && !need) {
+      ws.fresh[i] = state == 0 ? kNone : kBadEntry;
+      if (status) status[i] = state == 0 ? kOk : kBad;
     }
     int sum;
     const int excl = block_exclusive_sum<kScanThreads>(need, scratch, &sum);

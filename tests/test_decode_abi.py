@@ -138,6 +138,7 @@ def test_attention_refusals():
     _expect(call(page_size=0), BAD, "page_size")
     _expect(call(ld_table=3), BAD, "ld_table")
     _expect(call(max_pages=1 << 28, ld_table=1 << 28), UNS, "too many")
+    _expect(call(T=1 << 20, B=1 << 20, max_pages=1 << 16, ld_table=1 << 16), UNS, "row tiles")
     _expect(call(words=2), BAD, "ld_mask")
     _expect(call(qh=60), BAD, "strides")
     _expect(call(oh=62), BAD, "strides")

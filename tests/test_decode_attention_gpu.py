@@ -137,7 +137,7 @@ class Batch:
             g = lse.double().cpu().numpy()
             assert np.array_equal(np.isneginf(g), np.isneginf(want_lse))
             fine = np.isfinite(want_lse)
-            off = np.abs(g - want_lse)[fine] - (score + sums + 2.0 ** -18 + np.abs(np.where(fine, want_lse, 0)) * 2.0 ** -22)[fine]
+            off = np.abs(g[fine] - want_lse[fine]) - (score + sums + 2.0 ** -18 + np.abs(np.where(fine, want_lse, 0)) * 2.0 ** -22)[fine]
             assert off.size == 0 or off.max() <= 0, off.max()
 
 
@@ -162,6 +162,12 @@ CASES = [
     ([2], [33000], 4, 2, 256, 32, "bf16", "tree", False),
     ([4, 3], [10, 64], 8, 2, 128, 16, "f16", "none", False),
     ([2, 1], [0, 0], 4, 2, 64, 16, "bf16", "none", True),
+    # many rows over lines that are cut
+    ([40, 24], [3000, 500], 64, 8, 128, 16, "bf16", "tree", False),
+    ([20, 20], [1700, 90], 64, 8, 64, 16, "f16", "random", False),
+    ([1] * 300, list(range(0, 1500, 5)), 8, 8, 64, 16, "f16", "tree", False),
+    ([9] * 16, list(range(100, 1700, 100)), 16, 2, 256, 16, "bf16", "tree", False),
+    ([100, 90], [1500, 40], 16, 4, 80, 24, "f16", "tree", True),
 ]
 
 
