@@ -135,7 +135,9 @@ int lora_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_st
  * layer's keys are one pool, its values another); page p of a sequence holds
  * its positions [p page_size, (p + 1) page_size) in every pool.  A page is
  * free while its reference count is 0; it may belong to several sequences.
- * Only full pages are ever shared: a fork copies the last, partly filled one.
+ * Only full pages are ever shared: a fork copies the last, partly filled one,
+ * and a resize that cuts a sequence inside a shared page gives it its own.
+ * Slots of a page behind a sequence's tokens hold no defined bytes.
  *
  * A host struct whose pointers are caller-owned device buffers.  A table row
  * holds a sequence's page ids in its leading entries and -1 after them. */
@@ -180,8 +182,11 @@ typedef struct lora_page_cache {
 
 /* Sets sequence lengths and makes every row hold exactly the pages of its
  * length plus `extra` tokens to come: allocates what is missing, releases what
- * is too much.  lens [n] (NULL: lengths stay), extra [n] (NULL: 0), status [n]
- * (or NULL). */
+ * is too much.  With lens, a page at or behind the new end that another
+ * sequence holds as well (by the counts before the call) is replaced by one of
+ * the sequence's own, with a copy of the rows that stay filled; an entry that
+ * needs such a page and finds none is NO_SPACE like any other.  lens [n] (NULL:
+ * lengths stay), extra [n] (NULL: 0), status [n] (or NULL). */
 int lora_pages_resize(const lora_page_cache *cache, const int32_t *seqs, const int32_t *lens,
                       const int32_t *extra, int32_t n, int32_t *status, void *stream);
 

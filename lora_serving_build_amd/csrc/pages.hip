@@ -79,93 +79,6 @@ __device__ __forceinline__ int64_t pages_of(int64_t tokens, int page_size) {
   return (tokens + page_size - 1) / page_size;
 }
 
-// ---------------------------------------------------------------- resize
-__global__ void __launch_bounds__(kScanThreads) resize_kernel(PageView c, const int32_t* __restrict__ seqs,
-                                                              const int32_t* __restrict__ lens,
-                                                              const int32_t* __restrict__ extra, int n,
-                                                              int32_t* __restrict__ status) {
-  __shared__ int scratch[kScanThreads / kWave + 1];
-  __shared__ int32_t ids[kMaxPageEntries];
-  __shared__ int end[kMaxPageEntries];    // inclusive prefix of the pages needed
-  __shared__ int held[kMaxPageEntries];   // pages held before; -1: bad entry
-  __shared__ int want[kMaxPageEntries];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  for (int i = tid; i < n; i += kScanThreads) ids[i] = seqs[i];
-  __syncthreads();
-  for (int i = wave; i < n; i += kScanThreads / kWave) {
-    const int32_t s = ids[i];
-    bool same = false;
-    for (int j = lane; j < i; j += kWave) same |= ids[j] == s;
-    bool good = in_range(s, c.max_seqs) && !__any(same);
-    int have = 0;
-    int64_t need = 0;
-    if (good) {
-      const int32_t len = lens ? lens[i] : c.seq_len[s];
-      const int32_t more = extra ? extra[i] : 0;
-      need = pages_of((int64_t)len + more, c.page_size);
-      good = len >= 0 && more >= 0 && need <= c.max_pages;
-      if (good) have = row_pages(c.table + (int64_t)s * c.ld_table, c.max_pages);
-    }
-    if (lane == 0) {
-      held[i] = good ? have : -1;
-      want[i] = good ? (int)need : 0;
-    }
-  }
-  __syncthreads();
-  // Prefix sums of what each entry needs (a sum never passes 2^31: at most
-  // kMaxPageEntries rows of max_pages entries, which the host has checked).
-  int before = 0;
-  for (int base = 0; base < n; base += kScanThreads) {
-    const int i = base + tid;
-    const int need = i < n && held[i] >= 0 && want[i] > held[i] ? want[i] - held[i] : 0;
-    int sum;
-    const int excl = block_exclusive_sum<kScanThreads>(need, scratch, &sum);
-    if (i < n) end[i] = before + excl + need;
-    before += sum;
-  }
-  __syncthreads();
-  const int found = scan_free(c.refs, c.num_pages, before, scratch, [&](int rank, int32_t page) {
-    // The entry whose range of ranks holds this one.  Entries that turn out
-    // not to be served as a whole give their pages back below.
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (end[mid] > rank) hi = mid; else lo = mid + 1;
-    }
-    const int first = end[lo] - (want[lo] - held[lo]);
-    c.table[(int64_t)ids[lo] * c.ld_table + held[lo] + (rank - first)] = page;
-    c.refs[page] = 1;
-  });
-  __syncthreads();
-  for (int i = wave; i < n; i += kScanThreads / kWave) {
-    if (held[i] < 0) {
-      if (status && lane == 0) status[i] = kBad;
-      continue;
-    }
-    const int32_t s = ids[i];
-    int32_t* row = c.table + (int64_t)s * c.ld_table;
-    const bool grows = want[i] > held[i];
-    const bool fits = !grows || end[i] <= found;
-    // Release: the tail of a shrinking row, or the pages that an unserved
-    // entry received.
-    int from = want[i], to = held[i];
-    if (grows) {
-      const int first = end[i] - (want[i] - held[i]);
-      from = held[i];
-      to = fits || found <= first ? held[i] : held[i] + (found - first);
-    }
-    for (int w = from + lane; w < to; w += kWave) {
-      const int32_t p = row[w];
-      if (in_range(p, c.num_pages)) atomicSub(&c.refs[p], 1);
-      row[w] = -1;
-    }
-    if (lane == 0) {
-      if (lens && fits) c.seq_len[s] = lens[i];
-      if (status) status[i] = fits ? kOk : kNoSpace;
-    }
-  }
-}
-
 // ---------------------------------------------------------------- copies
 // Whole pages are moved 16 bytes a lane, past the caches' normal replacement:
 // nothing here reads them again.  One block moves one piece of kPiece bytes with
@@ -190,6 +103,182 @@ __global__ void __launch_bounds__(256) copy_kernel(PageView c, const int32_t* __
   if (!in_range(a, c.num_pages) || !in_range(b, c.num_pages) || a == b || at >= page_bytes) return;
   uint8_t* pool = c.pool + blockIdx.z * c.pool_stride + at;
   store_row(pool + b * c.page_stride, load_row(pool + a * c.page_stride));
+}
+
+// ---------------------------------------------------------------- resize
+// A page at or behind a sequence's new end that other sequences hold too (the
+// row was forked and is cut now) is replaced by one of the sequence's own, so
+// that no append reaches the others; the one that the end lies in keeps its
+// filled rows.  Counts as they were before the call decide, so entries that cut
+// the same page at once each get their own.  A fresh page that still has to
+// receive rows is marked by its count, ~(page to copy from), until the second
+// kernel has copied them; its last slot, which is not filled, holds a note.
+// Calls in a row, with lengths and without (one launch less): 7.1 and 4.2 us for
+// one entry, 8.8 and 5.2 for 48, 26 and 20 for 256.  48 branches cut inside a
+// shared page, 101 MB read and written in 64 pools: 47 us.
+struct CutNote {
+  int32_t done;   // blocks that have copied their part
+  int32_t entry;  // whose page it is
+};
+
+__device__ __forceinline__ CutNote* cut_note(const PageView& c, int32_t page) {
+  return reinterpret_cast<CutNote*>(c.pool + page * c.page_stride + (c.page_size - 1) * c.row_bytes);
+}
+
+__global__ void __launch_bounds__(kScanThreads) resize_kernel(PageView c, const int32_t* __restrict__ seqs,
+                                                              const int32_t* __restrict__ lens,
+                                                              const int32_t* __restrict__ extra, int n,
+                                                              int32_t* __restrict__ status) {
+  __shared__ int scratch[kScanThreads / kWave + 1];
+  __shared__ int32_t ids[kMaxPageEntries];
+  __shared__ int end[kMaxPageEntries];    // inclusive prefix of the pages needed
+  __shared__ int held[kMaxPageEntries];   // pages held before; -1: bad entry
+  __shared__ int want[kMaxPageEntries];
+  __shared__ int cut[kMaxPageEntries];    // first entry of the row that is replaced
+  __shared__ int own[kMaxPageEntries];    // how many are
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  for (int i = tid; i < n; i += kScanThreads) ids[i] = seqs[i];
+  __syncthreads();
+  for (int i = wave; i < n; i += kScanThreads / kWave) {
+    const int32_t s = ids[i];
+    bool same = false;
+    for (int j = lane; j < i; j += kWave) same |= ids[j] == s;
+    bool good = in_range(s, c.max_seqs) && !__any(same);
+    int have = 0;
+    int64_t need = 0;
+    if (good) {
+      const int32_t len = lens ? lens[i] : c.seq_len[s];
+      const int32_t more = extra ? extra[i] : 0;
+      need = pages_of((int64_t)len + more, c.page_size);
+      good = len >= 0 && more >= 0 && need <= c.max_pages;
+      if (good) have = row_pages(c.table + (int64_t)s * c.ld_table, c.max_pages);
+    }
+    if (lane == 0) {
+      held[i] = good ? have : -1;
+      want[i] = good ? (int)need : 0;
+      own[i] = 0;
+    }
+  }
+  __syncthreads();
+  if (lens) {
+    // A thread looks at an entry that keeps one such page, a wave at one that
+    // keeps more (room for many tokens to come).
+    auto kept = [&](int i) { return min(held[i], want[i]); };
+    auto shared = [&](int i, int w) {
+      const int32_t p = c.table[(int64_t)ids[i] * c.ld_table + w];
+      return in_range(p, c.num_pages) && c.refs[p] > 1;
+    };
+    for (int i = tid; i < n; i += kScanThreads) {
+      cut[i] = held[i] < 0 ? 0 : lens[i] / c.page_size;
+      if (cut[i] + 1 == kept(i)) own[i] = shared(i, cut[i]);
+    }
+    __syncthreads();
+    for (int i = wave; i < n; i += kScanThreads / kWave) {
+      if (cut[i] + 1 >= kept(i)) continue;
+      int last = cut[i] - 1;
+      for (int w0 = cut[i]; w0 < kept(i); w0 += kWave) {
+        const uint64_t m = __ballot(w0 + lane < kept(i) && shared(i, w0 + lane));
+        if (m) last = w0 + kWave - 1 - __clzll((long long)m);
+      }
+      if (lane == 0) own[i] = last - cut[i] + 1;
+    }
+    __syncthreads();
+  }
+  auto needs = [&](int i) { return held[i] < 0 ? 0 : own[i] + max(want[i] - held[i], 0); };
+  // Prefix sums of what each entry needs (a sum never passes 2^31: at most
+  // kMaxPageEntries rows of max_pages entries, which the host has checked).
+  int before = 0;
+  for (int base = 0; base < n; base += kScanThreads) {
+    const int i = base + tid;
+    const int need = i < n ? needs(i) : 0;
+    int sum;
+    const int excl = block_exclusive_sum<kScanThreads>(need, scratch, &sum);
+    if (i < n) end[i] = before + excl + need;
+    before += sum;
+  }
+  __syncthreads();
+  // Where the r-th page that entry i receives goes in its row.
+  auto place = [&](int i, int r) { return r < own[i] ? cut[i] + r : held[i] + r - own[i]; };
+  const int found = scan_free(c.refs, c.num_pages, before, scratch, [&](int rank, int32_t page) {
+    // The entry whose range of ranks holds this one.  Entries that turn out
+    // not to be served as a whole give their pages back below.
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (end[mid] > rank) hi = mid; else lo = mid + 1;
+    }
+    const int r = rank - (end[lo] - needs(lo));
+    int32_t* at = c.table + (int64_t)ids[lo] * c.ld_table + place(lo, r);
+    c.refs[page] = r < own[lo] ? ~*at : 1;
+    *at = page;
+  });
+  __syncthreads();
+  for (int i = wave; i < n; i += kScanThreads / kWave) {
+    if (held[i] < 0) {
+      if (status && lane == 0) status[i] = kBad;
+      continue;
+    }
+    const int32_t s = ids[i];
+    int32_t* row = c.table + (int64_t)s * c.ld_table;
+    const int need = needs(i), got = min(max(found - (end[i] - need), 0), need);
+    const bool fits = got == need;
+    if (fits) {
+      for (int r = lane; r < own[i]; r += kWave) {
+        const int32_t page = row[cut[i] + r], old = ~c.refs[page];
+        const bool there = in_range(old, c.num_pages);
+        if (there) atomicSub(&c.refs[old], 1);
+        if (r == 0 && there && lens[i] % c.page_size != 0)
+          *cut_note(c, page) = CutNote{0, i};
+        else
+          c.refs[page] = 1;
+      }
+      for (int w = want[i] + lane; w < held[i]; w += kWave) {  // the tail of a shrinking row
+        const int32_t p = row[w];
+        if (in_range(p, c.num_pages)) atomicSub(&c.refs[p], 1);
+        row[w] = -1;
+      }
+    } else {
+      for (int r = lane; r < got; r += kWave) {  // what an unserved entry received
+        int32_t* at = row + place(i, r);
+        const int32_t page = *at;
+        *at = r < own[i] ? ~c.refs[page] : -1;
+        c.refs[page] = 0;
+      }
+    }
+    if (lane == 0) {
+      if (lens && fits) c.seq_len[s] = lens[i];
+      if (status) status[i] = fits ? kOk : kNoSpace;
+    }
+  }
+}
+
+// Blocks (i, 0 .. kCutBlocks - 1), which deal out the pools: the filled rows of
+// the page that entry i's sequence was cut in, from the page that it gave up.
+// Most entries have none: four dependent look-ups, and few blocks to make them.
+// The last block to finish clears the mark, which the others have read by then.
+constexpr int kCutBlocks = 8;
+
+__global__ void __launch_bounds__(256) resize_copy_kernel(PageView c, const int32_t* __restrict__ seqs) {
+  const int i = blockIdx.x;
+  const int32_t s = seqs[i];
+  if (!in_range(s, c.max_seqs)) return;
+  const int32_t len = c.seq_len[s];
+  const int w = len / c.page_size, rest = len % c.page_size;
+  if (rest <= 0 || w >= c.max_pages) return;
+  const int32_t fresh = c.table[(int64_t)s * c.ld_table + w];
+  if (!in_range(fresh, c.num_pages)) return;
+  const int32_t old = ~c.refs[fresh];
+  if (!in_range(old, c.num_pages)) return;
+  CutNote* note = cut_note(c, fresh);
+  if (note->entry != i) return;  // a later entry that repeats the sequence
+  const int per_chunk = (int)(rest * c.row_bytes / 16);
+  for (int pool = blockIdx.y; pool < c.num_pools; pool += gridDim.y)
+    for (int e = threadIdx.x; e < per_chunk * c.chunks; e += 256) {
+      uint8_t* at = c.pool + pool * c.pool_stride + e / per_chunk * (c.page_size * c.row_bytes) + (int64_t)(e % per_chunk) * 16;
+      store_row(at + fresh * c.page_stride, load_row(at + old * c.page_stride));
+    }
+  __syncthreads();
+  if (threadIdx.x == 0 && atomicAdd(&note->done, 1) == (int)gridDim.y - 1) c.refs[fresh] = 1;
 }
 
 // ---------------------------------------------------------------- fork
@@ -522,6 +611,9 @@ size_t compact_workspace(int32_t num_pages) { return 3 * (size_t)num_pages * 4 +
 hipError_t launch_pages_resize(const PageView& c, const int32_t* seqs, const int32_t* lens, const int32_t* extra,
                                int32_t n, int32_t* status, hipStream_t s) {
   resize_kernel<<<1, kScanThreads, 0, s>>>(c, seqs, lens, extra, n, status);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !lens) return e;  // a sequence that keeps its length is cut in no page
+  resize_copy_kernel<<<dim3(n, c.num_pools < kCutBlocks ? c.num_pools : kCutBlocks), 256, 0, s>>>(c, seqs);
   return hipGetLastError();
 }
 

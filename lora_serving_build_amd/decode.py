@@ -352,8 +352,9 @@ class PageCache:
 def lora_pages_resize(cache: PageCache, seqs: torch.Tensor, lens: torch.Tensor | None = None,
                       extra: torch.Tensor | None = None, status: torch.Tensor | None = None) -> None:
     """Sets the sequences' lengths (lens; None: as they are) and makes their
-    rows hold exactly the pages of length + extra tokens.  status (optional):
-    PAGES_OK, PAGES_NO_SPACE or PAGES_BAD for each."""
+    rows hold exactly the pages of length + extra tokens.  A sequence that lens
+    cuts inside a page which others hold too gets its own copy of it.  status
+    (optional): PAGES_OK, PAGES_NO_SPACE or PAGES_BAD for each."""
     n = _count(seqs, "seqs")
     at = _gpu(cache.pool, seqs, lens, extra, status)
     _run(_base.lib().lora_pages_resize(cache._ref, _int32(seqs, "seqs", n),
