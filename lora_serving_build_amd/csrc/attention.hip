@@ -672,9 +672,13 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
         for (int i = 0; i < PASS; ++i) *reinterpret_cast<u32x4*>(&kt[n & 1][(prow + i * RPP) * KP + piece]) = reg[i];
       }
     };
+    // Whether tile n lies in the context and all of its positions exist: only the
+    // other tiles are looked at, and can have notes.
+    auto plain = [&](int n, uint64_t there) {
+      return begin + (n + 1) * KEYS <= it.s.ctx && (KEYS == 64 ? !~there : (uint32_t)there == ~0u);
+    };
     auto stash_values = [&](int n, uint64_t there) {
-      const bool plain = begin + (n + 1) * KEYS <= it.s.ctx && (KEYS == 64 ? !~there : (uint32_t)there == ~0u);
-      if (!plain) {
+      if (!plain(n, there)) {
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
@@ -784,11 +788,12 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
       // between two barriers, and only where there can be any.
       stash_values(n + 1, there1);
+      const bool noted = !plain(n, there0);
       there0 = there1;
       there1 = there2;
       there2 = note_rows(n + 3, later);
       __syncthreads();
-      if (begin + (n + 1) * KEYS > it.s.ctx) {
+      if (noted) {
         if (tid < KEYS / 32) odd_rows[n & 1][tid] = 0;
         __syncthreads();
       }
