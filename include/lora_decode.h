@@ -88,7 +88,8 @@ int lora_q4_matmul(const void *x, int64_t ldx, const lora_q4_weight *w, int32_t 
  * over the positions p that node i sees.  A row that sees nothing is 0 and its
  * lse is -inf.  What a row does not see never reaches it, NaN and infinities
  * among it.  Scores, the softmax and the sums are fp32; the weights are rounded
- * to the cache's type before they meet v; o is rounded once. */
+ * to the cache's type before they meet v (in f16 those below 2^-23 of the row's
+ * heaviest to fewer bits, 2^-33 of it being the last); o is rounded once. */
 typedef struct lora_tree_batch {
   int32_t B;                 /* sequences                                           */
   int32_t T;                 /* rows of q; start[B] = T                             */

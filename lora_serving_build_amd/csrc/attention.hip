@@ -289,12 +289,20 @@ __device__ __forceinline__ void mask_scores(uint32_t seen, int quad, f32x4 (&s)[
       if (!((seen >> (t * 16 + quad * 4 + e)) & 1)) s[t][e] = -INFINITY;
 }
 
+// log2 of what a weight of 1 stands for, from the row's reference score m.  In
+// binary16 that is 2^9 below the reference, so that the weights use the upper end
+// of the type's range (2^15 at most, see weigh) and those far below the heaviest
+// are not lost while the sum l counts them: from 2^-23 of the reference down
+// they have fewer bits, and the last step is 2^-33 of it.
+template <int DT>
+__device__ __forceinline__ float weight_base(float m, float c) { return __builtin_fmaf(m, c, DT == 0 ? -9.f : 0.f); }
+
 // One step of the running softmax of RT row tiles: raw scores in, weights out
 // (and as the 16-bit operands of the value product).  c = |scale| log2 e.  The
 // reference scores m follow the maxima only when one has grown by 2^6 in
-// weight: until then the weights are at most 64, which loses nothing in fp32
-// sums and saves the scaling of l and o.  One branch for all row tiles: their
-// chains of dependent operations run side by side.
+// weight: until then the weights are at most 2^6 of the reference's, which loses
+// nothing in fp32 sums and saves the scaling of l and o.  One branch for all row
+// tiles: their chains of dependent operations run side by side.
 template <int DT, int RT, int N>
 __device__ __forceinline__ void weigh(f32x4 (&s)[RT][2], float c, float (&m)[RT], float (&l)[RT], f32x4 (&o)[RT][N],
                                       u32x4 (&w)[RT]) {
@@ -320,7 +328,7 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[RT][2], float c, float (&m)[RT]
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    const float base = m[r] == -INFINITY ? 0.f : -m[r] * c;
+    const float base = m[r] == -INFINITY ? 0.f : -weight_base<DT>(m[r], c);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
     l[0] += __shfl_xor(l[0], 16);
     l[0] += __shfl_xor(l[0], 32);
     if (quad == 0) {
-      row_max[wave][col] = m[0] * c;
+      row_max[wave][col] = weight_base<DT>(m[0], c);
       row_sum[wave][col] = l[0];
     }
     __syncthreads();  // every wave is done with its values
@@ -810,7 +818,7 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
       sum += __shfl_xor(sum, 32);
       const int in_tile = (wave * RT + r) * 16 + col, row = row0 + r * 16 + col;
       if (row >= rows) continue;
-      const float top = m[r] * c, base = m[r] == -INFINITY ? 0.f : top;
+      const float top = weight_base<DT>(m[r], c), base = m[r] == -INFINITY ? 0.f : top;
       if (slot) {
 #pragma unroll
         for (int d = 0; d < OT; ++d) *reinterpret_cast<f32x4*>(slot + in_tile * DP + d * 16 + quad * 4) = o[r][d];
