@@ -87,9 +87,12 @@ int lora_q4_matmul(const void *x, int64_t ldx, const lora_q4_weight *w, int32_t 
  *   w_p = exp(scale q[i, h] . k[p, h / G]),  G = heads / kv_heads,
  * over the positions p that node i sees.  A row that sees nothing is 0 and its
  * lse is -inf.  What a row does not see never reaches it, NaN and infinities
- * among it.  Scores, the softmax and the sums are fp32; the weights are rounded
- * to the cache's type before they meet v (in f16 those below 2^-23 of the row's
- * heaviest to fewer bits, 2^-33 of it being the last); o is rounded once. */
+ * among it.  Scores, the softmax and the sums are fp32; o is rounded once.  The
+ * matrix cores take the weights in 16 bits: as a sum of two parts, which adds
+ * little to o's own rounding, for dims up to 128 and up to 64 rows (nodes times
+ * G) a sequence on average; beyond that rounded once to the cache's type.  In
+ * f16 a weight below 2^-23 of the row's heaviest keeps fewer bits, 2^-33 of that
+ * one being the last. */
 typedef struct lora_tree_batch {
   int32_t B;                 /* sequences                                           */
   int32_t T;                 /* rows of q; start[B] = T                             */

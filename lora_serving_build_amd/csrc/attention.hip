@@ -211,13 +211,38 @@ __device__ __forceinline__ u32x2 lds_read_transposed(const uint16_t* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p)));
 }
 
+// Whether one of the 8 N values is an infinity or NaN: the largest magnitude's
+// pattern tells (in four chains, since a wave may be alone on its SIMD).
+template <int DT, int N>
+__device__ __forceinline__ bool not_finite(const u32x4 (&v)[N]) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 most[4] = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      most[x] = __builtin_elementwise_max(most[x], __builtin_bit_cast(u16x2, v[i][x] & 0x7fff7fffu));
+  most[0] = __builtin_elementwise_max(__builtin_elementwise_max(most[0], most[1]), __builtin_elementwise_max(most[2], most[3]));
+  const unsigned short e = DT == 0 ? 0x7c00 : 0x7f80;
+  return most[0].x >= e || most[0].y >= e;
+}
 template <int DT>
 __device__ __forceinline__ bool not_finite(u32x4 v) {
-  const uint32_t e = DT == 0 ? 0x7c00u : 0x7f80u;
-  bool bad = false;
+  const u32x4 one[1] = {v};
+  return not_finite<DT, 1>(one);
+}
+
+// Rows of a step (a bit each) to which `lanes` of its i-th load of VL belong.
+template <int VL>
+__device__ __forceinline__ uint32_t rows_of(int i, uint64_t lanes) {
+  constexpr int RPL = kKeys / VL, LPR = kWave / RPL;
+  uint32_t rows = 0;
+  if (lanes) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x) bad |= (v[x] & e) == e || ((v[x] >> 16) & e) == e;
-  return bad;
+    for (int x = 0; x < RPL; ++x)
+      if ((lanes >> (x * LPR)) & ((1ull << LPR) - 1ull)) rows |= 1u << (i * RPL + x);
+  }
+  return rows;
 }
 
 // pos / page_size for 0 <= pos < 2^31: the high half of a product with
@@ -297,15 +322,25 @@ __device__ __forceinline__ void mask_scores(uint32_t seen, int quad, f32x4 (&s)[
 template <int DT>
 __device__ __forceinline__ float weight_base(float m, float c) { return __builtin_fmaf(m, c, DT == 0 ? -9.f : 0.f); }
 
+// 16-bit parts in which a weight meets the values.  Two (the weight rounded, and
+// what that left over) leave o with little more than its own rounding, and are
+// free where the kernels wait for memory: 64 sequences of one token 115 us with
+// two and 117 with one, 64 rows 79 and 79.  With 128 rows they would cost a sixth
+// (dim 128: 152 us against 130, dim 64: 108 against 92), with dim 256 up to a
+// third (16 rows: 197 against 154, for want of registers): there a weight is
+// rounded once, to the cache's type.
+template <int DP, int ROWS>
+constexpr int weight_parts() { return DP <= 128 && ROWS <= 64 ? 2 : 1; }
+
 // One step of the running softmax of RT row tiles: raw scores in, weights out
 // (and as the 16-bit operands of the value product).  c = |scale| log2 e.  The
 // reference scores m follow the maxima only when one has grown by 2^6 in
 // weight: until then the weights are at most 2^6 of the reference's, which loses
 // nothing in fp32 sums and saves the scaling of l and o.  One branch for all row
 // tiles: their chains of dependent operations run side by side.
-template <int DT, int RT, int N>
+template <int DT, int PARTS, int RT, int N>
 __device__ __forceinline__ void weigh(f32x4 (&s)[RT][2], float c, float (&m)[RT], float (&l)[RT], f32x4 (&o)[RT][N],
-                                      u32x4 (&w)[RT]) {
+                                      u32x4 (&w)[PARTS][RT]) {
   float top[RT];
   bool grown = false;
 #pragma unroll
@@ -336,23 +371,35 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[RT][2], float c, float (&m)[RT]
         s[r][t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t][e], c, base));
         l[r] += s[r][t][e];
       }
-    w[r] = u32x4{cvt_pack2<DT>(s[r][0].x, s[r][0].y), cvt_pack2<DT>(s[r][0].z, s[r][0].w),
-                 cvt_pack2<DT>(s[r][1].x, s[r][1].y), cvt_pack2<DT>(s[r][1].z, s[r][1].w)};
+    w[0][r] = u32x4{cvt_pack2<DT>(s[r][0].x, s[r][0].y), cvt_pack2<DT>(s[r][0].z, s[r][0].w),
+                    cvt_pack2<DT>(s[r][1].x, s[r][1].y), cvt_pack2<DT>(s[r][1].z, s[r][1].w)};
+    if constexpr (PARTS == 2) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float a, b;
+        unpack2<DT>(w[0][r][x], &a, &b);
+        w[1][r][x] = cvt_pack2<DT>(s[r][x / 2][x % 2 * 2] - a, s[r][x / 2][x % 2 * 2 + 1] - b);
+      }
+    }
   }
 }
 
 // Adds the value row p (position i of the step), which is not finite
 // throughout and was kept out of the products, to the rows that see it.
-template <int DT, int N>
-__device__ __forceinline__ void add_odd_value(const uint16_t* p, int i, int dim, int col, int quad, u32x4 w,
-                                              f32x4 (&o)[N]) {
+template <int DT, int PARTS, int RT, int N>
+__device__ __forceinline__ void add_odd_value(const uint16_t* p, int i, int dim, int col, int quad,
+                                              const u32x4 (&w)[PARTS][RT], int r, f32x4 (&o)[N]) {
   // Weight of position 16 t + 4 q + e: lane (q, col), half e % 2 of dword 2 t + e / 2.
-  uint32_t two = 0;
+  float weight = 0.f;
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
-    if (i / 16 * 2 + i % 4 / 2 == x) two = w[x];
-  two = __shfl(two, (i % 16 / 4) * 16 + col);
-  const float weight = to_f32<DT>(i % 2 ? two >> 16 : two & 0xffffu);
+  for (int part = 0; part < PARTS; ++part) {
+    uint32_t two = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i / 16 * 2 + i % 4 / 2 == x) two = w[part][r][x];
+    two = __shfl(two, (i % 16 / 4) * 16 + col);
+    weight += to_f32<DT>(i % 2 ? two >> 16 : two & 0xffffu);
+  }
 #pragma unroll
   for (int d = 0; d < N; ++d) {
     __builtin_amdgcn_sched_barrier(0);  // one load at a time: registers count, time does not
@@ -396,6 +443,7 @@ __device__ __forceinline__ void store_quad(const AttnArgs& a, int t, int h, int 
 template <int DT, int DP, int W, bool WHOLE>
 __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a) {
   constexpr int ROWS = 16, TILE = W * kKeys;
+  constexpr int PARTS = weight_parts<DP, ROWS>();
   constexpr int KS = DP / 32;             // matrix-core steps of a score
   constexpr int OT = DP / 16;             // tiles of the output's columns
   constexpr int PITCH = DP + 16;          // of a staged value row, in elements: rows start 8 banks apart
@@ -482,28 +530,36 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
         for (int s = 0; s < KS; ++s) sc[0][t] = mfma16x16x32<DT>(k[t][s], q[s], sc[0][t]);
       }
 
-      // Values that are not finite are kept out of the products with weight 0:
-      // they are staged as 0 and added below to the rows that see them.
+      // Values that are not finite are kept out of the products, where a weight
+      // of 0 (not seen) or below 0 (what rounding left over) would make NaN of
+      // them: their rows are staged as 0 and added below to the rows that see
+      // them.  With one part, whose weights are never below 0, only steps are
+      // looked at in which rows differ in what they see.
       uint32_t odd = 0;  // positions of the step with such values
       const bool drafted = key0 + kKeys > it.s.ctx;
-      if (drafted || there != 0xffffffffu) {
+      if (there != 0xffffffffu || (PARTS == 1 && drafted)) {
 #pragma unroll
         for (int i = 0; i < VL; ++i) {
           const int r = i * RPL + lane / LPR;
-          const bool zero = !((there >> r) & 1);
-          const uint64_t lanes = __ballot(not_finite<DT>(v[i]) && !zero);
-          if (drafted && lanes) {
-#pragma unroll
-            for (int x = 0; x < RPL; ++x)
-              if ((lanes >> (x * LPR)) & ((1ull << LPR) - 1ull)) odd |= 1u << (i * RPL + x);
+          bool zero = !((there >> r) & 1);
+          if (PARTS == 1 && drafted) {
+            odd |= rows_of<VL>(i, __ballot(not_finite<DT>(v[i]) && !zero));
+            zero |= (odd >> r) & 1;
           }
-          if (zero || ((odd >> r) & 1)) v[i] = u32x4{0u, 0u, 0u, 0u};
+          if (zero) v[i] = u32x4{0u, 0u, 0u, 0u};
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      uint16_t* mine = stage + lane / LPR * PITCH + lane % LPR * 8;
 #pragma unroll
-      for (int i = 0; i < VL; ++i)
-        *reinterpret_cast<u32x4*>(stage + (i * RPL + lane / LPR) * PITCH + lane % LPR * 8) = v[i];
+      for (int i = 0; i < VL; ++i) *reinterpret_cast<u32x4*>(mine + i * RPL * PITCH) = v[i];
+      if (PARTS == 2 && __any(not_finite<DT>(v))) {
+#pragma unroll
+        for (int i = 0; i < VL; ++i) {
+          odd |= rows_of<VL>(i, __ballot(not_finite<DT>(v[i])));
+          if ((odd >> (i * RPL + lane / LPR)) & 1) *reinterpret_cast<u32x4*>(mine + i * RPL * PITCH) = u32x4{0u, 0u, 0u, 0u};
+        }
+      }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
       // The next step.
@@ -513,8 +569,8 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
       page = page_of(next + TILE);
 
       if (drafted || there != 0xffffffffu) mask_scores(seen_bits(a, it, node, word, key0, there), quad, sc[0]);
-      u32x4 w[1];
-      weigh<DT, 1, OT>(sc, c, m, l, o, w);
+      u32x4 w[PARTS][1];
+      weigh<DT, PARTS, 1, OT>(sc, c, m, l, o, w);
 
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -522,14 +578,16 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
         // Elements 0..3: positions 4 quad + 0..3 of the first 16, 4..7 of the second.
         const uint16_t* p = stage + (quad * 4 + (col >> 2)) * PITCH + d * 16 + (col & 3) * 4;
         const u32x2 lo = lds_read_transposed(p), hi = lds_read_transposed(p + 16 * PITCH);
-        o[0][d] = mfma16x16x32<DT>(u32x4{lo.x, lo.y, hi.x, hi.y}, w[0], o[0][d]);
+        const u32x4 vf = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) o[0][d] = mfma16x16x32<DT>(vf, w[part][0], o[0][d]);
       }
       __builtin_amdgcn_wave_barrier();
 
       while (odd) {
         const int i = __ffs(odd) - 1;
         odd &= odd - 1;
-        add_odd_value<DT, OT>(vbase + __shfl(here, i), i, a.dim, col, quad, w[0], o[0]);
+        add_odd_value<DT>(vbase + __shfl(here, i), i, a.dim, col, quad, w, 0, o[0]);
       }
     }
 
@@ -597,6 +655,7 @@ template <int DT, int DP, int RT>
 __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnArgs a) {
   constexpr int ROWS = kWaves * 16 * RT;
   constexpr int KEYS = wide_tile<DP>();
+  constexpr int PARTS = weight_parts<DP, ROWS>();
   constexpr int KS = DP / 32, OT = DP / 16;
   constexpr int KP = DP + 8, VP = DP + 16;   // pitches: key rows 4 banks apart, value rows 8
   constexpr int CPR = DP / 8;                // 16-byte pieces of a row
@@ -669,7 +728,8 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
     };
     // Tile n's keys and values on their way into the registers, and from there
     // into its buffer.  Value rows that do not exist are staged as 0; so are
-    // those of drafted nodes that are not finite, which are noted.
+    // those that are not finite, which are noted (with weights in one part, which
+    // are never below 0, only where rows differ in what they see).
     auto fetch = [&](int n, const uint16_t* base) {
 #pragma unroll
       for (int i = 0; i < PASS; ++i) reg[i] = *reinterpret_cast<const u32x4*>(base + where[n & 3][prow + i * RPP]);
@@ -680,20 +740,17 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
         for (int i = 0; i < PASS; ++i) *reinterpret_cast<u32x4*>(&kt[n & 1][(prow + i * RPP) * KP + piece]) = reg[i];
       }
     };
-    // Whether tile n lies in the context and all of its positions exist: only the
-    // other tiles are looked at, and can have notes.
-    auto plain = [&](int n, uint64_t there) {
-      return begin + (n + 1) * KEYS <= it.s.ctx && (KEYS == 64 ? !~there : (uint32_t)there == ~0u);
-    };
+    auto all_there = [](uint64_t there) { return KEYS == 64 ? !~there : (uint32_t)there == ~0u; };
+    // Whether every row sees all of tile n.
+    auto plain = [&](int n, uint64_t there) { return begin + (n + 1) * KEYS <= it.s.ctx && all_there(there); };
     auto stash_values = [&](int n, uint64_t there) {
-      if (!plain(n, there)) {
-        bool bad = false;
+      if (PARTS == 2 || !plain(n, there)) {
+        if (PARTS == 1 || !all_there(there)) {
 #pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-          if (!((there >> (prow + i * RPP)) & 1)) reg[i] = u32x4{0u, 0u, 0u, 0u};
-          bad |= not_finite<DT>(reg[i]);
+          for (int i = 0; i < PASS; ++i)
+            if (!((there >> (prow + i * RPP)) & 1)) reg[i] = u32x4{0u, 0u, 0u, 0u};
         }
-        if (__builtin_expect(__any(bad), 0)) {
+        if (__builtin_expect(__any(not_finite<DT>(reg)), 0)) {
 #pragma unroll
           for (int i = 0; i < PASS; ++i) {
             const int r = prow + i * RPP, first = lane / CPR * CPR;
@@ -778,25 +835,27 @@ __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnAr
           vf[d] = u32x4{lo.x, lo.y, hi.x, hi.y};
         }
         __builtin_amdgcn_sched_barrier(0);
-        u32x4 w[RT];
-        weigh<DT, RT, OT>(sc, c, m, l, o, w);
+        u32x4 w[PARTS][RT];
+        weigh<DT, PARTS, RT, OT>(sc, c, m, l, o, w);
 #pragma unroll
-        for (int d = 0; d < OT; ++d)
+        for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf[d], w[r], o[r][d]);
+          for (int d = 0; d < OT; ++d)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) o[r][d] = mfma16x16x32<DT>(vf[d], w[part][r], o[r][d]);
         uint32_t odd = odd_rows[n & 1][half];
         while (__builtin_expect(odd != 0, 0)) {
           const int i = __ffs(odd) - 1;
           odd &= odd - 1;
           const uint16_t* p = vhead + where[n & 3][half * 32 + i];
 #pragma unroll
-          for (int r = 0; r < RT; ++r) add_odd_value<DT, OT>(p, i, a.dim, col, quad, w[r], o[r]);
+          for (int r = 0; r < RT; ++r) add_odd_value<DT>(p, i, a.dim, col, quad, w, r, o[r]);
         }
       }
-      // Buffer n & 1 is free after the barrier.  Its notes of odd rows are cleared
-      // between two barriers, and only where there can be any.
+      // Buffer n & 1 is free after the barrier.  Its notes of odd rows, which every
+      // wave reads before, are cleared between two barriers where there are any.
       stash_values(n + 1, there1);
-      const bool noted = !plain(n, there0);
+      const bool noted = __builtin_amdgcn_readfirstlane(odd_rows[n & 1][0] | odd_rows[n & 1][KEYS / 32 - 1]) != 0;
       there0 = there1;
       there1 = there2;
       there2 = note_rows(n + 3, later);

@@ -105,3 +105,37 @@ def test_lse_of_single_positions(dtype):
     b.check(out, lse)
     v = torch.stack([b.v[position(b, s, 0)] for s in (0, 0, 1)]).repeat_interleave(2, 1)
     assert torch.equal(out, v)
+
+
+@pytest.mark.parametrize("nodes,ctx,heads,kv,dim,page", [
+    ([1], [509], 32, 8, 128, 16), ([2], [700], 8, 1, 96, 16), ([1, 1, 1], [31, 320, 3300], 8, 2, 64, 16),
+    ([3, 2], [5000, 40], 8, 2, 80, 24), ([40], [1500], 4, 4, 128, 16), ([33, 17], [500, 900], 2, 1, 64, 16),
+    ([12], [1100], 8, 2, 72, 32),
+])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_weights_in_two_parts(nodes, ctx, heads, kv, dim, page, dtype):
+    """Up to 64 rows a sequence, of dims up to 128, the weights' rounding does not
+    show in o: the tolerance has its square (what two 16-bit parts leave over) in
+    its place."""
+    b = Batch(nodes, ctx, heads, kv, dim, page, dtype, seed=dim + sum(ctx))
+    got = b.run()
+    o, _, mag, spread = b.expect()
+    half = torch.finfo(DT[dtype]).eps / 2
+    sums, score = (64 + max(ctx) / 128) * 2.0 ** -23, (spread * (dim + 8) * 2.0 ** -23)[..., None]
+    tol = np.abs(o) * half * 1.001 + mag * (half * half + 2 * score + 2 * sums + 2.0 ** -20 + (max(ctx) + 64) * 2.0 ** -34) + 2.0 ** -24
+    assert np.max(np.abs(got.double().cpu().numpy() - o) / tol) <= 1
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("nodes", [2, 12])
+def test_infinite_value_with_a_small_weight(nodes, dtype):
+    """A drafted node's infinite value reaches the rows that see it, whatever its
+    weight, and its finite columns have both parts of the weight."""
+    b = Batch([nodes], [300], 8, 2, 128, 16, dtype, mask="chain", seed=nodes)
+    p = position(b, 0, 300)
+    b.v[p][1, 7] = float("inf")
+    got = b.run()
+    assert bool(torch.isposinf(got[:, 4:, 7]).all())
+    b.v[p][1, 7] = 0.0
+    got[:, 4:, 7] = torch.from_numpy(b.expect()[0][:, 4:, 7]).to(got)
+    b.check(got)
