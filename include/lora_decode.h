@@ -225,8 +225,10 @@ int lora_pages_fork(const lora_page_cache *cache, const int32_t *src, const int3
  * from position seq_len on; row path[i][j] moves to row j, j < accepted[i], in
  * every pool, and new_len[i] = seq_len + the rows kept (seq_len itself is set
  * by a resize).  path is [n][ld_path], columns <= LORA_MAX_PATH; a path ends at
- * its first entry that is not above the one before it or not below
- * drafted[i].  seqs are distinct.  new_len must not overlap seq_len. */
+ * its first entry that is not above the one before it, not below drafted[i], or
+ * whose row or place has no page (a draft that found no space); what is behind
+ * it is not kept.  seqs are distinct; new_len of one out of range is 0.  new_len
+ * must not overlap seq_len. */
 int lora_pages_accept(const lora_page_cache *cache, const int32_t *seqs, const int32_t *drafted,
                       const int32_t *path, int64_t ld_path, int32_t columns, const int32_t *accepted,
                       int32_t n, int32_t *new_len, void *stream);

@@ -476,29 +476,33 @@ __global__ void __launch_bounds__(256) accept_kernel(PageView c, const int32_t* 
     if (p <= before || p >= bound) atomicMin(&ends, j);
   }
   __syncthreads();
-  const int kept = ends;
-  if (blockIdx.y == 0 && tid == 0) new_len[i] = len + kept;
-  // The rows that move, by the first wave; the table is read for all of them at
-  // once (entries without a move look at the row's first entry).
+  // The rows that move, by the first wave, up to the first row or place without a
+  // page; the table is read for 64 of them at once (entries beyond the row look
+  // at its first entry).
   if (tid < kWave) {
-    int64_t moves = 0;
+    int kept = ends, moves = 0;
     for (int j0 = 0; j0 < kept; j0 += kWave) {
       const int j = j0 + tid;
       const int32_t p = mine[min(j, kept - 1)];
       const int64_t fp = ((int64_t)len + p) / c.page_size, tp = ((int64_t)len + j) / c.page_size;
-      bool ok = j < kept && p != j && len >= 0 && fp < c.max_pages;
+      const bool in = len >= 0 && fp < c.max_pages && tp < c.max_pages;
       const int32_t* row = c.table + (int64_t)s * c.ld_table;
-      const int32_t a = row[ok ? fp : 0], b = row[ok ? tp : 0];
-      ok = ok && in_range(a, c.num_pages) && in_range(b, c.num_pages);
-      const uint64_t m = __ballot(ok);
-      if (ok) {
-        const int at = (int)moves + __popcll(m & ((1ull << tid) - 1ull));
+      const int32_t a = row[in ? fp : 0], b = row[in ? tp : 0];
+      const uint64_t none = __ballot(j < kept && !(in && in_range(a, c.num_pages) && in_range(b, c.num_pages)));
+      if (none) kept = j0 + __ffsll((unsigned long long)none) - 1;
+      const bool move = j < kept && p != j;
+      const uint64_t m = __ballot(move);
+      if (move) {
+        const int at = moves + __popcll(m & ((1ull << tid) - 1ull));
         from[at] = a * c.page_stride + ((int64_t)len + p) % c.page_size * c.row_bytes;
         to[at] = b * c.page_stride + ((int64_t)len + j) % c.page_size * c.row_bytes;
       }
       moves += __popcll(m);
     }
-    if (tid == 0) ends = (int)moves;
+    if (tid == 0) {
+      if (blockIdx.y == 0) new_len[i] = len + kept;
+      ends = moves;
+    }
   }
   __syncthreads();
   const int moves = ends;

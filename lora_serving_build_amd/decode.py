@@ -413,8 +413,9 @@ def lora_pages_fork(cache: PageCache, src: torch.Tensor, dst: torch.Tensor, stat
 def lora_pages_accept(cache: PageCache, seqs: torch.Tensor, drafted: torch.Tensor, path: torch.Tensor,
                       accepted: torch.Tensor, new_len: torch.Tensor) -> torch.Tensor:
     """Moves the accepted nodes' rows (path int32 [n][columns], accepted[i] of
-    them) to the front of each sequence's drafted rows, in every pool.  new_len
-    receives seq_len + the rows kept; a resize with it makes that the length."""
+    them) to the front of each sequence's drafted rows, in every pool, up to the
+    first that has no page.  new_len receives seq_len + the rows kept; a resize
+    with it makes that the length."""
     n = _count(seqs, "seqs")
     if path.dtype is not _I32 or path.dim() != 2:
         raise ValueError("path must be an int32 [n][columns] tensor with contiguous rows")
