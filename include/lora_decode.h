@@ -30,7 +30,7 @@ extern "C" {
  * W[c, h] = scale[c, h / group] * (q[c, h] - zero[c, h / group]),
  * with 4-bit codes q in [0, 15].  Without zeros, zero = 8.  The products are
  * exact (16-bit x times a small whole number), sums and scales are fp32, and y
- * is rounded once. */
+ * is rounded once.  Infinities and NaN in x give what the definition gives. */
 
 /* A weight as lora_q4_pack lays it out.  A host struct whose pointer is a
  * caller-owned device buffer. */

@@ -41,7 +41,7 @@ struct Q4Args {
   int64_t ldx;
   const uint8_t* packed;
   int64_t scales_at, zeros_at;  // zeros_at = 0: every zero is 8
-  int32_t n, k, tiles, blocks;
+  int32_t n, k, tiles, blocks, sub;
   int32_t T;
   uint16_t* y;
   int64_t ldy;

@@ -81,6 +81,7 @@ hipError_t launch_q4_matmul(const uint16_t* x, int64_t ldx, const void* packed, 
   a.k = k;
   a.tiles = lay.tiles;
   a.blocks = lay.blocks;
+  a.sub = lay.sub;
   a.T = T;
   a.y = y;
   a.ldy = ldy;

@@ -116,6 +116,63 @@ __device__ __forceinline__ Q4Scale<DT> q4_scale(u32x2 scales, uint32_t z) {
   return r;
 }
 
+// bfloat16 takes (128 + z) sum x away from sum (128 + q) x.  Where x is infinite
+// or its sums pass fp32's range that is inf - inf, although sum (q - z) x is an
+// infinity with a sign, or in range.  Results that are not finite are therefore
+// taken again, from the definition, in 64 bits.  That costs nothing where all are
+// finite, little where a token has a NaN (which decides all of its results), and
+// milliseconds where one has infinities (4 for 28672 x 8192).
+__device__ __forceinline__ bool q4_finite(f32x4 r) {
+  return fabsf(r.x) + fabsf(r.y) + fabsf(r.z) + fabsf(r.w) < INFINITY;
+}
+
+// Outputs c .. c + 3 (those below n) of token t for the lanes that need them.
+// Every lane of the wave calls it.
+__device__ __forceinline__ f32x4 q4_again(const Q4Args& a, int lane, bool needed, int t, int c) {
+  bool nan = false;
+  for (uint64_t left = __ballot(needed); left;) {  // token after token
+    const int token = __builtin_amdgcn_readlane(t, __ffsll((unsigned long long)left) - 1);
+    const uint16_t* x = a.x + (int64_t)token * a.ldx;
+    bool found = false;
+    for (int h0 = 0; h0 < a.k && !__any(found); h0 += 16 * kWave)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) found |= (x[min(h0 + j * kWave + lane, a.k - 1)] & 0x7fffu) > 0x7f80u;
+    nan |= __any(found) && t == token;
+    left &= ~__ballot(t == token);
+  }
+  if (!needed) return f32x4{0.f, 0.f, 0.f, 0.f};
+  if (nan) return f32x4{NAN, NAN, NAN, NAN};
+  const uint16_t* x = a.x + (int64_t)t * a.ldx;
+  const int per_scale = 128 / a.sub;
+  f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int e = 0; e < 4 && c + e < a.n; ++e) {
+    const int tile = (c + e) / 16, row = (c + e) % 16;
+    double sum = 0;
+#pragma unroll 1
+    for (int h0 = 0; h0 < a.k && sum == sum; h0 += 8) {
+      // Eight inputs: a dword as packed, one scale.
+      const int64_t unit = (int64_t)tile * a.blocks + h0 / 128;
+      const int in = h0 % 128, w = in / 32, quad = in / 8 % 4;
+      const uint32_t d = reinterpret_cast<const uint32_t*>(a.packed)[unit * 256 + (row + 16 * quad) * 4 + w];
+      const int64_t at = (unit * a.sub + in / per_scale) * 16 + row;
+      const int z = a.zeros_at ? a.packed[a.zeros_at + at] : 8;
+      const float scale = to_f32<1>(reinterpret_cast<const uint16_t*>(a.packed + a.scales_at)[at]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = h0 + j < a.k ? to_f32<1>(x[h0 + j]) : 0.f;
+        const int q = (d >> (j / 2 * 4 + j % 2 * 16)) & 15u;
+        if (h0 + j < a.k) sum += (double)((float)(q - z) * scale) * (double)v;
+      }
+    }
+    if (e == 0) r.x = (float)sum;
+    if (e == 1) r.y = (float)sum;
+    if (e == 2) r.z = (float)sum;
+    if (e == 3) r.w = (float)sum;
+  }
+  return r;
+}
+
 // Outputs c .. c + 3 of token t (those below n).
 template <int DT>
 __device__ __forceinline__ void q4_store(const Q4Args& a, int t, int c, f32x4 r) {
@@ -239,7 +296,15 @@ __global__ void __launch_bounds__(kWavesPerTile* kWave) q4_kernel(Q4Args a) {
     f32x4 r = sums[0][mi][l];
 #pragma unroll
     for (int w = 1; w < W; ++w) r += sums[w][mi][l];
-    if (t < a.T) q4_store<DT>(a, t, (tile0 + m) * 16 + (l >> 4) * 4, r);
+    const int c = (tile0 + m) * 16 + (l >> 4) * 4;
+    if constexpr (DT == 1) {
+      const bool again = t < a.T && c < a.n && !q4_finite(r);
+      if (__any(again)) {
+        const f32x4 exact = q4_again(a, l, again, t, c);
+        if (again) r = exact;
+      }
+    }
+    if (t < a.T) q4_store<DT>(a, t, c, r);
   }
 }
 
@@ -258,7 +323,10 @@ __global__ void __launch_bounds__(kWavesPerTile* kWave) q4_kernel(Q4Args a) {
 // the scaling of the sub-groups' sums.
 constexpr int kShareWaves = 8;
 
-template <int DT, int SUB, bool ZEROS, int MT, int NT>
+// AGAIN: results that are not finite are taken again here (bfloat16 without
+// splits; with splits the kernel that adds them does it, and this one keeps its
+// registers: 128 tokens, groups of 64: 39 us against 44).
+template <int DT, int SUB, bool ZEROS, int MT, int NT, bool AGAIN>
 __global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared_kernel(Q4Args a, int splits) {
   constexpr int CB = NT >= 8 ? 1 : 8 / NT;  // blocks of a chunk: up to 32 KiB of x
   constexpr int OPS = CB * NT * 4;          // operands of 16 tokens x 32 inputs
@@ -387,6 +455,7 @@ __global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared
     __syncthreads();
   }
 
+  uint32_t again = 0;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = (tile0 + m) * 16 + quad * 4;
@@ -395,10 +464,22 @@ __global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared
     for (int i = 0; i < NT; ++i) {
       const int t = t0 + i * 16 + col;
       if (t >= a.T) continue;
-      if (splits > 1)
+      if (!AGAIN && splits > 1)
         *reinterpret_cast<f32x4*>(a.partial + ((int64_t)split * a.T + t) * (a.tiles * 16) + row) = acc[m][i];
-      else
+      else if (!AGAIN || q4_finite(acc[m][i]))
         q4_store<DT>(a, t, row, acc[m][i]);
+      else
+        again |= 1u << (m * NT + i);
+    }
+  }
+  if constexpr (AGAIN) {
+#pragma unroll 1
+    for (int mi = 0; mi < MT * NT && __any(again >> mi); ++mi) {
+      const bool mine = (again >> mi) & 1;
+      if (!__any(mine)) continue;
+      const int row = (tile0 + mi / NT) * 16 + quad * 4, t = t0 + mi % NT * 16 + col;
+      const f32x4 exact = q4_again(a, lane, mine, t, row);
+      if (mine) q4_store<DT>(a, t, row, exact);
     }
   }
 }
@@ -408,13 +489,20 @@ __global__ void __launch_bounds__(kShareWaves* kWave, NT <= 2 ? 4 : 2) q4_shared
 template <int DT>
 __global__ void __launch_bounds__(256) q4_add_kernel(Q4Args a, int splits) {
   const int c = (blockIdx.y * 256 + threadIdx.x) * 4, t = blockIdx.x;
-  if (c >= a.n) return;
+  const bool in = c < a.n;
   const int64_t width = (int64_t)a.tiles * 16;
-  const float* p = a.partial + t * width + c;
+  const float* p = a.partial + t * width + (in ? c : 0);
   f32x4 sum = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll 4
   for (int s = 1; s < splits; ++s) sum += *reinterpret_cast<const f32x4*>(p + s * a.T * width);
-  q4_store<DT>(a, t, c, sum);
+  if constexpr (DT == 1) {
+    const bool again = in && !q4_finite(sum);
+    if (__any(again)) {
+      const f32x4 exact = q4_again(a, threadIdx.x & (kWave - 1), again, t, c);
+      if (again) sum = exact;
+    }
+  }
+  if (in) q4_store<DT>(a, t, c, sum);
 }
 
 // ---------------------------------------------------------------- launch
@@ -496,7 +584,10 @@ template <int DT, int SUB, bool ZEROS, int MT, int NT>
 hipError_t launch_shared(const Q4Args& a, int splits, hipStream_t s) {
   const int groups = (a.tiles + MT * kShareWaves - 1) / (MT * kShareWaves);
   const dim3 grid(groups * splits, (a.T + 16 * NT - 1) / (16 * NT));
-  q4_shared_kernel<DT, SUB, ZEROS, MT, NT><<<grid, kShareWaves * kWave, 0, s>>>(a, splits);
+  if (DT == 1 && splits == 1)
+    q4_shared_kernel<DT, SUB, ZEROS, MT, NT, DT == 1><<<grid, kShareWaves * kWave, 0, s>>>(a, splits);
+  else
+    q4_shared_kernel<DT, SUB, ZEROS, MT, NT, false><<<grid, kShareWaves * kWave, 0, s>>>(a, splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   q4_add_kernel<DT><<<dim3(a.T, (a.n + 1023) / 1024), 256, 0, s>>>(a, splits);

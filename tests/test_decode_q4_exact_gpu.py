@@ -1,4 +1,7 @@
-"""4-bit products whose every sum is exact, compared bit for bit: x and the scales are powers of two or small whole numbers, so each
+"""4-bit products whose every sum is exact, compared bit for bit, and products
+of infinities and of very large inputs.
+
+Exact sums: x and the scales are powers of two or small whole numbers, so each
 partial sum is a whole number below 2^24 times one power of two, in whatever
 order it is taken; y is its rounding."""
 import numpy as np
@@ -74,3 +77,49 @@ def test_exact_sums(T, n, k, group, zeros, dtype):
         part[:, lo] = 1.0
         assert torch.equal(product(part, codes, scales, z, k, group),
                            expected(part, codes, scales, z, k, group, dtype)), (lo, hi)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,n,k,group,zeros", [s for s in SHAPES if s[0] * s[1] * s[2] < 2e9])
+def test_infinities(T, n, k, group, zeros, dtype):
+    """Infinite inputs give what the definition gives: an infinity of the sign
+    of (q - z) x, NaN where q = z or where infinities of both signs meet."""
+    x, codes, scales, z = whole(T, n, k, group, zeros, dtype, seed=T + n)
+    inf = float("inf")
+    x[0, k - 1] = inf
+    if T > 3:
+        x[1, k // 2] = -inf
+        x[2, 0], x[2, k - 1] = inf, inf
+        x[3, 0], x[3, k // 3] = inf, float("nan")
+    if T > 20:
+        x[T - 1, 3], x[T - 1, k - 2] = inf, -inf
+    ref = reference(torch.where(torch.isfinite(x), x, 0), codes, scales, z, k, group, dtype)[0]
+    unit = torch.eye(k, dtype=x.dtype, device="cuda")[~torch.isfinite(x).all(0)]  # the inputs that are not finite somewhere
+    w = dict(zip(torch.nonzero(~torch.isfinite(x).all(0))[:, 0].tolist(), reference(unit, codes, scales, z, k, group, dtype)[0]))
+    with np.errstate(invalid="ignore"):
+        for t, h in torch.nonzero(~torch.isfinite(x)).tolist():
+            ref[t] += w[h] * float(x[t, h])
+    got = product(x, codes, scales, z, k, group).double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    there = ~np.isnan(ref)
+    assert np.array_equal(got[there], torch.from_numpy(ref).to(DT[dtype]).double().numpy()[there])
+    assert np.isposinf(ref[0]).any() and np.isneginf(ref[0]).any()
+    old = torch.full((T, n), 3.0, dtype=x.dtype, device="cuda")
+    lsb.lora_q4_matmul(x, lsb.lora_q4_pack(codes, scales, z, k, group), old, add_inputs=True)
+    added = old.double().cpu().numpy()
+    far = ~np.isfinite(ref)
+    assert np.array_equal(added[far], got[far], equal_nan=True)
+    assert np.array_equal(added[~far], torch.from_numpy(ref + 3.0).to(x.dtype).double().numpy()[~far])
+
+
+@pytest.mark.parametrize("T,n,k,group,zeros", [(1, 64, 1024, 128, True), (6, 512, 4096, 64, False), (40, 8192, 1024, 32, True),
+                                               (58, 505, 16888, 32, True)])
+def test_very_large_inputs(T, n, k, group, zeros):
+    """bfloat16 inputs near the type's end whose products with the weights are
+    far below it."""
+    x, codes, scales, z = whole(T, n, k, group, zeros, "bf16", seed=n)
+    scales = scales * 2.0 ** -20
+    big = x * 2.0 ** 125                                # |x| up to 2^126, the sums of x beyond 2^128
+    ref = reference(x, codes, scales, z, k, group, "bf16")[0] * 2.0 ** 125
+    got = product(big, codes, scales, z, k, group)
+    assert torch.equal(got, torch.from_numpy(ref).cuda().to(torch.bfloat16))
