@@ -145,6 +145,12 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+def _ld(rows: int, stride: int, width: int) -> int:
+    """Row stride as the library takes it: that of a lone row means nothing.
+    Rows that overlap keep theirs, which the library refuses."""
+    return stride if rows > 1 else max(stride, width)
+
+
 def _gpu(*tensors) -> int:
     """Index of the GPU that holds all of the tensors (None: not given)."""
     at = tensors[0].get_device()
@@ -297,10 +303,10 @@ def lora_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         (mask_rows, words), (ld_mask, mask_in) = mask.shape, mask.stride()
         if mask_rows < T or (mask_in != 1 and words > 1):
             raise ValueError("mask must be an int64 [T][words] tensor with contiguous rows")
-        mask_ptr, ld_mask = mask.data_ptr(), max(ld_mask, words)
+        mask_ptr, ld_mask = mask.data_ptr(), _ld(mask_rows, ld_mask, words)
     at = _gpu(q, k_cache, v_cache, table, ctx_len, start, out, mask, lse, workspace)
     batch = _BATCH(B, T, _int32(start, "start", B + 1), _int32(ctx_len, "ctx_len", B), table.data_ptr(),
-                   max(ld_table, max_pages), max_pages, mask_ptr, ld_mask, words)
+                   _ld(B, ld_table, max_pages), max_pages, mask_ptr, ld_mask, words)
     layer = _LAYER(k_cache.data_ptr(), v_cache.data_ptr(), page_st, token_st, head_st, num_pages, page_size)
     stream = _raw_stream(at)
     L = _base.lib()
@@ -339,7 +345,7 @@ class PageCache:
         self.num_pages, self.max_pages = pages, max_pages
         self.c = _CPageCache(pool.data_ptr(), pool.stride(0) * 2, pool.stride(1) * 2,
                              dim * 2 if head_major else b * dim * 2, a if head_major else 1, pools, pages,
-                             self.page_size, refs_ptr, table.data_ptr(), max(table.stride(0), max_pages), max_seqs,
+                             self.page_size, refs_ptr, table.data_ptr(), _ld(max_seqs, table.stride(0), max_pages), max_seqs,
                              max_pages, len_ptr)
         self._ref = ctypes.addressof(self.c)
 
@@ -424,7 +430,7 @@ def lora_pages_accept(cache: PageCache, seqs: torch.Tensor, drafted: torch.Tenso
         raise ValueError("path must be an int32 [n][columns] tensor with contiguous rows")
     at = _gpu(cache.pool, seqs, drafted, path, accepted, new_len)
     _run(_base.lib().lora_pages_accept(cache._ref, _int32(seqs, "seqs", n), _int32(drafted, "drafted", n),
-                                       path.data_ptr(), max(ld_path, columns), columns,
+                                       path.data_ptr(), _ld(rows, ld_path, columns), columns,
                                        _int32(accepted, "accepted", n), n, _int32(new_len, "new_len", n),
                                        _raw_stream(at)))
     return new_len
