@@ -239,9 +239,13 @@ _ws_cache: dict = {}
 
 def _workspace(device: torch.device, nbytes: int) -> torch.Tensor | None:
     """A workspace per (device, stream), grown on demand.  Calls on one stream
-    run in order, so they can share it."""
+    run in order, so they can share it.  A call that is captured in a graph gets
+    a new one from the graph's own memory: graphs may be replayed side by side,
+    and outlive a buffer that grows."""
     if nbytes == 0:
         return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=device)
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:

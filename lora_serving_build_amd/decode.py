@@ -4,6 +4,9 @@ over a paged cache, and the cache's page operations.
 
 Argument marshalling only, as in the package's ``__init__``: shapes, strides,
 dtype codes and the current stream of torch tensors.
+
+Calls that need a workspace take ``workspace``, or use one that is kept for the
+current stream.  Captured in a graph they take it from the graph's memory.
 """
 from __future__ import annotations
 
@@ -128,6 +131,7 @@ def _run(rc: int) -> None:
 # on the GPU than here on the host: checks take the cheapest accessors
 # (get_device, identity of dtypes), structs are packed in one go.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 _I32, _U8, _F32, _I64 = torch.int32, torch.uint8, torch.float32, torch.int64
 
 
@@ -178,14 +182,16 @@ def _count(t: torch.Tensor, name: str) -> int:
 
 
 def _workspace(at: int, stream: int, nbytes: int, given: torch.Tensor | None):
-    """Address and size of a call's workspace: the one given, or the stream's."""
+    """A call's workspace, its address and size: the one given, or the stream's
+    (in a captured call: one of its own, from the graph's memory)."""
     if given is None:
         if nbytes == 0:
-            return None, 0
-        given = _base._ws_cache.get((at, stream))
+            return None, None, 0
+        if not _capturing():
+            given = _base._ws_cache.get((at, stream))
         if given is None or given.numel() < nbytes:
             given = _base._workspace(torch.device("cuda", at), nbytes)
-    return given.data_ptr(), given.numel() * given.element_size()
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 # ---------------------------------------------------------------- 4-bit products
@@ -252,7 +258,7 @@ def lora_q4_matmul(x: torch.Tensor, w: Q4Weight, y: torch.Tensor, add_inputs: bo
     at = _gpu(w.packed, x, y, workspace)
     stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(at, stream, L.lora_q4_matmul_workspace_bytes(T, n, k, w.group), workspace)
+    held, ws, ws_bytes = _workspace(at, stream, L.lora_q4_matmul_workspace_bytes(T, n, k, w.group), workspace)
     _run(L.lora_q4_matmul(x.data_ptr(), ldx, w._ref, T, y.data_ptr(), ldy, 1 if add_inputs else 0, ws, ws_bytes, stream))
     return y
 
@@ -310,7 +316,7 @@ def lora_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     layer = _LAYER(k_cache.data_ptr(), v_cache.data_ptr(), page_st, token_st, head_st, num_pages, page_size)
     stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(at, stream, L.lora_tree_attention_workspace_bytes(B, T, heads, kv_heads, dim), workspace)
+    held, ws, ws_bytes = _workspace(at, stream, L.lora_tree_attention_workspace_bytes(B, T, heads, kv_heads, dim), workspace)
     _run(L.lora_tree_attention(q.data_ptr(), q_token, q_head, layer, batch, heads, kv_heads, dim, scale,
                                out.data_ptr(), o_token, o_head, lse.data_ptr() if lse is not None else None, ws,
                                ws_bytes, code, stream))
@@ -411,7 +417,7 @@ def lora_pages_fork(cache: PageCache, src: torch.Tensor, dst: torch.Tensor, stat
     at = _gpu(cache.pool, src, dst, status, workspace)
     stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(at, stream, L.lora_pages_fork_workspace_bytes(n, cache.max_pages), workspace)
+    held, ws, ws_bytes = _workspace(at, stream, L.lora_pages_fork_workspace_bytes(n, cache.max_pages), workspace)
     _run(L.lora_pages_fork(cache._ref, _int32(src, "src", n), _int32(dst, "dst", n), n,
                            _int32(status, "status", n) if status is not None else None, ws, ws_bytes, stream))
 
@@ -453,6 +459,6 @@ def lora_pages_compact(cache: PageCache, live: torch.Tensor, workspace: torch.Te
     at = _gpu(cache.pool, live, workspace)
     stream = _raw_stream(at)
     L = _base.lib()
-    ws, ws_bytes = _workspace(at, stream, L.lora_pages_compact_workspace_bytes(cache.num_pages), workspace)
+    held, ws, ws_bytes = _workspace(at, stream, L.lora_pages_compact_workspace_bytes(cache.num_pages), workspace)
     _run(L.lora_pages_compact(cache._ref, _int32(live, "live", 1), ws, ws_bytes, stream))
     return live
