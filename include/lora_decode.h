@@ -96,7 +96,8 @@ int lora_q4_matmul(const void *x, int64_t ldx, const lora_q4_weight *w, int32_t 
 typedef struct lora_tree_batch {
   int32_t B;                 /* sequences                                           */
   int32_t T;                 /* rows of q; start[B] = T                             */
-  const int32_t *start;      /* [B + 1] ascending from 0                            */
+  const int32_t *start;      /* [B + 1] ascending from 0; where it does not ascend, */
+                             /* what out and lse hold afterwards is undefined       */
   const int32_t *ctx_len;    /* [B] tokens of the context                           */
   const int32_t *table;      /* [B][ld_table] page ids; positions of pages outside  */
   int64_t ld_table;          /* [0, num_pages) are not seen                         */

@@ -28,9 +28,11 @@ struct Seq {
   int n, q0, ctx, len;  // nodes, first row, context, positions
 };
 
-__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+// descends (optional): set if the sequence ends before it starts.
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool* descends = nullptr) {
   Seq s;
   const int lo = min(max(a.start[b], 0), a.T), hi = min(max(a.start[b + 1], 0), a.T);
+  if (descends) *descends |= hi < lo;
   s.q0 = lo;
   s.n = max(hi - lo, 0);
   const int64_t most = (int64_t)a.max_pages * a.page_size;
@@ -114,7 +116,10 @@ __device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
   const int part = (blockIdx.x & 7) * (kParts / 8) + (blockIdx.x >> 3);
   auto lines_of = [&](const Seq& s) { return row_tiles(s.n, group, ROWS) * a.kv_heads; };
   // Sequence base + lane, empty beyond the last; the first 64 are read once.
-  auto read = [&](int base) { return base + lane < a.B ? sequence(a, base + lane) : Seq{0, 0, 0, 0}; };
+  bool descends = false;
+  auto read = [&](int base) {
+    return base + lane < a.B ? sequence(a, base + lane, &descends) : Seq{0, 0, 0, 0};
+  };
   const Seq head = read(0);
   auto seq_at = [&](int base) { return base == 0 ? head : read(base); };
   uint32_t lines = 0, tiles = 0;
@@ -123,6 +128,12 @@ __device__ __forceinline__ bool find_part(const AttnArgs& a, Place* p) {
     const int l = lines_of(s);
     lines += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(l), kWave - 1);
     tiles += (uint32_t)__builtin_amdgcn_readlane(wave_inclusive_sum(l * key_tiles(s.len, KEYS)), kWave - 1);
+  }
+  // Starts that do not ascend can name more rows than there are, and 32 bits may
+  // not hold their tiles: there are no parts, and nothing to join (cost 0).
+  if (__any(descends)) {
+    if (part == 0 && threadIdx.x == 0) space(a).part[0] = 0;
+    return false;
   }
   // With fewer tiles than parts every tile is a part.
   const int cost = tiles <= (uint32_t)kParts ? 0 : COST;
@@ -924,6 +935,7 @@ __global__ void __launch_bounds__(kJoinWaves* kWave) join_kernel(AttnArgs a) {
   if (b < 0) return;
   const Seq s = sequence(a, b);
   const int part_cost = sp.part[0], cost = sp.part[1];
+  if (part_cost == 0) return;
   const int tiles = key_tiles(s.len, KEYS), rts = row_tiles(s.n, group, ROWS);
   const int row = (t - s.q0) * group + head % group, rt = row / ROWS, in_tile = row % ROWS;
   const int tiles0 = sp.first[b] + (head / group * rts + rt) * (cost + tiles) + cost;
@@ -1018,6 +1030,7 @@ __global__ void __launch_bounds__(kWaves* kWave) join_lines_kernel(AttnArgs a) {
   if (!find_line<ROWS, KEYS>(a, &it)) return;
   const Space sp = space(a);
   const int part_cost = sp.part[0], cost = sp.part[1];
+  if (part_cost == 0) return;
   const int tiles0 = sp.first[it.b] + (it.h * it.rts + it.rt) * (cost + it.tiles) + cost;
   const int part0 = tiles0 / part_cost, splits = min((tiles0 + it.tiles - 1) / part_cost, kParts - 1) - part0 + 1;
   if (splits < 2) return;
