@@ -55,8 +55,8 @@ size_t lora_q4_packed_bytes(int32_t n, int32_t k, int32_t group, int has_zeros);
  *   w       host; filled by the call
  *   packed  16-byte aligned, packed_bytes >= lora_q4_packed_bytes
  * Errors: INVALID_ARG (NULL, n or k < 1, strides, dtype), UNSUPPORTED (group
- * not a multiple of 32, sizes whose packed form passes 2^40 bytes), WORKSPACE
- * (packed_bytes too small or unaligned), HIP. */
+ * not a multiple of 32, n above 2^27 - 16, more than 2^24 - 1 blocks of 16 outputs
+ * x 128 inputs), WORKSPACE (packed_bytes too small or unaligned), HIP. */
 int lora_q4_pack(const uint8_t *codes, int64_t ld_codes, const void *scales, int64_t ld_scales,
                  const uint8_t *zeros, int64_t ld_zeros, int32_t n, int32_t k, int32_t group,
                  int dtype, void *packed, size_t packed_bytes, lora_q4_weight *w, void *stream);
@@ -126,7 +126,8 @@ typedef struct lora_kv_layer {
  * Same inputs give the same bits.
  * Errors: INVALID_ARG (NULL, sizes, strides, alignment, dtype), UNSUPPORTED
  * (dim; a table row of more than 2^31 - 256 positions; 2^31 or more units of 16
- * rows, a key head and 32 positions of the table), WORKSPACE, HIP. */
+ * rows, a key head and 32 positions of the table; launches of 2^32 threads),
+ * WORKSPACE, HIP. */
 size_t lora_tree_attention_workspace_bytes(int32_t B, int32_t T, int32_t heads, int32_t kv_heads,
                                            int32_t dim);
 int lora_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -183,7 +184,8 @@ typedef struct lora_page_cache {
  * that needs one is served.  Pages released by a call are given out by later
  * calls only.  Table entries outside [0, num_pages) are never followed.
  * Errors of each: INVALID_ARG (NULL, sizes, strides, alignment), UNSUPPORTED
- * (n or another size above its limit), WORKSPACE, HIP. */
+ * (n or another size above its limit; T of an append or max_seqs of a compaction
+ * above 2^24 - 1), WORKSPACE, HIP. */
 
 /* Sets sequence lengths and makes every row hold exactly the pages of its
  * length plus `extra` tokens to come: allocates what is missing, releases what

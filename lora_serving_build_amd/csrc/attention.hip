@@ -1106,10 +1106,11 @@ __global__ void __launch_bounds__(kWaves* kWave) join_lines_kernel(AttnArgs a) {
 
 // Most lines a call can have: every sequence has at most one row tile that is
 // not full.
-int64_t line_bound(const AttnArgs& a, int tile_rows) {
-  const int64_t rows = (int64_t)a.T * (a.heads / a.kv_heads);
-  return (rows / tile_rows + (a.B < rows ? a.B : rows)) * a.kv_heads;
+int64_t line_bound(int32_t B, int32_t T, int32_t heads, int32_t kv_heads, int tile_rows) {
+  const int64_t rows = (int64_t)T * (heads / kv_heads);
+  return (rows / tile_rows + (B < rows ? B : rows)) * kv_heads;
 }
+int64_t line_bound(const AttnArgs& a, int tile_rows) { return line_bound(a.B, a.T, a.heads, a.kv_heads, tile_rows); }
 
 // ROWS = 16: the kernel for few rows; 64, 128: the one for many.
 template <int DT, int DP, int ROWS>
@@ -1134,11 +1135,14 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
 // Whether the table holds so few positions that a workgroup of eight waves takes
 // each line whole: 509 positions, one token, 32 heads: 8.7 us and 3.9 us of the
 // join's launch in parts.
-bool short_lines(const AttnArgs& a) { return (int64_t)a.max_pages * a.page_size <= kShortLine; }
+bool short_lines(int64_t positions) { return positions <= kShortLine; }
+
+// Waves of a workgroup that takes whole lines: what the registers allow.
+constexpr int short_waves(int dp) { return dp == 256 ? 4 : 8; }
 
 template <int DT, int DP>
 hipError_t launch_short(const AttnArgs& a, hipStream_t s) {
-  constexpr int W = DP == 256 ? 4 : 8;  // what the registers allow
+  constexpr int W = short_waves(DP);
   attention_kernel<DT, DP, W, true><<<(unsigned)line_bound(a, 16), W * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -1158,7 +1162,8 @@ int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 template <int DT, int DP>
 hipError_t launch_rows(const AttnArgs& a, int rows, hipStream_t s) {
-  if (rows == 16) return short_lines(a) ? launch_short<DT, DP>(a, s) : launch<DT, DP, 16>(a, s);
+  if (rows == 16)
+    return short_lines((int64_t)a.max_pages * a.page_size) ? launch_short<DT, DP>(a, s) : launch<DT, DP, 16>(a, s);
   if constexpr (DP != 256) {
     if (rows == 128) return launch<DT, DP, 128>(a, s);
   }
@@ -1173,6 +1178,12 @@ hipError_t launch_dt(const AttnArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t attention_threads(int32_t B, int32_t T, int32_t heads, int32_t kv_heads, int32_t dim, int64_t positions) {
+  const int dp = padded_dim(dim), rows = choose_rows(B, T, heads / kv_heads, dp);
+  const int waves = rows == 16 && short_lines(positions) ? short_waves(dp) : kWaves;
+  return line_bound(B, T, heads, kv_heads, rows) * waves * kWave;
+}
 
 size_t attention_workspace(int32_t B, int32_t T, int32_t heads, int32_t kv_heads, int32_t dim) {
   const int dp = padded_dim(dim), rows = choose_rows(B, T, heads / kv_heads, dp);

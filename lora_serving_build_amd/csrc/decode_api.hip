@@ -23,6 +23,9 @@ int check_workspace(const void* workspace, size_t given, size_t need, const char
 }
 
 // ---------------------------------------------------------------- 4-bit products
+// A launch has at most 2^32 - 1 threads in x: this many workgroups of `threads`.
+constexpr int64_t most_blocks(int threads) { return 0xffffffffll / threads; }
+
 // Shape of a weight; LORA_OK if its packed form can exist.
 int check_q4(int32_t n, int32_t k, int32_t group, int dtype, const char* fn) {
   if (dtype != LORA_F16 && dtype != LORA_BF16)
@@ -30,8 +33,10 @@ int check_q4(int32_t n, int32_t k, int32_t group, int dtype, const char* fn) {
   if (n < 1 || k < 1) return fail(LORA_ERR_INVALID_ARG, "%s: n %d and k %d must be at least 1", fn, n, k);
   if (group < 32 || group % 32 != 0)
     return fail(LORA_ERR_UNSUPPORTED, "%s: group %d is not a multiple of 32", fn, group);
-  // The grid of the packing kernel is one workgroup per (16 outputs, 128 inputs).
-  if ((((int64_t)n + 15) / 16) * (((int64_t)k + 127) / 128) > 0x7fffffff || n > 0x7fffffff - 16 || k > 0x7fffffff - 128)
+  // The packing kernel has a workgroup of 256 for each (16 outputs, 128 inputs),
+  // the products one of 512 for each 16 outputs at most.
+  const int64_t tiles = ((int64_t)n + 15) / 16, units = tiles * (((int64_t)k + 127) / 128);
+  if (units > most_blocks(256) || tiles > most_blocks(512) || k > 0x7fffffff - 128)
     return fail(LORA_ERR_UNSUPPORTED, "%s: n %d x k %d is too large", fn, n, k);
   return LORA_OK;
 }
@@ -177,6 +182,7 @@ int lora_pages_append(const lora_page_cache* cache, int32_t k_pool, int32_t v_po
       !aligned(k, 16) || !aligned(v, 16))
     return fail(LORA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned with strides that are multiples of 8", fn);
   if (n == 0 || T == 0) return ok();
+  if (T > most_blocks(256)) return fail(LORA_ERR_UNSUPPORTED, "%s: T %d is too large", fn, T);
   if (!k || !v || !seqs || !start) return fail(LORA_ERR_INVALID_ARG, "%s: k, v, seqs and start must not be NULL", fn);
   const lora::AppendArgs a{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_token_stride,
                            k_head_stride, v_token_stride, v_head_stride, k_pool, v_pool, heads, dim, seqs, start, n};
@@ -247,6 +253,8 @@ int lora_pages_compact(const lora_page_cache* cache, int32_t* live, void* worksp
   static const char* fn = "lora_pages_compact";
   lora::PageView v;
   if (int e = check_cache(cache, fn, &v)) return e;
+  if (v.max_seqs > most_blocks(256))
+    return fail(LORA_ERR_UNSUPPORTED, "%s: %d rows of the table are too many", fn, v.max_seqs);
   if (!live) return fail(LORA_ERR_INVALID_ARG, "%s: live must not be NULL", fn);
   if (int e = check_workspace(workspace, workspace_bytes, lora::compact_workspace(v.num_pages), fn)) return e;
   return hip_status(lora::launch_pages_compact(v, live, workspace, static_cast<hipStream_t>(stream)), fn);
@@ -291,6 +299,8 @@ int lora_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   if (b.B == 0 || b.T == 0) return ok();
   if (!q || !out || !b.start || !b.ctx_len || (b.max_pages > 0 && !b.table) || (c.num_pages > 0 && (!c.k || !c.v)))
     return fail(LORA_ERR_INVALID_ARG, "%s: q, out, start, ctx_len, table, k and v must not be NULL", fn);
+  if (lora::attention_threads(b.B, b.T, heads, kv_heads, dim, (int64_t)b.max_pages * c.page_size) > 0xffffffffll)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: %lld row tiles are too many", fn, (long long)(tiles * kv_heads));
   if (int e = check_workspace(workspace, workspace_bytes,
                               lora::attention_workspace(b.B, b.T, heads, kv_heads, dim), fn))
     return e;

@@ -133,6 +133,8 @@ struct AttnArgs {
   float* partial;      // workspace
 };
 
+// Threads of the call's largest launch, of a table of `positions` in a row.
+int64_t attention_threads(int32_t B, int32_t T, int32_t heads, int32_t kv_heads, int32_t dim, int64_t positions);
 size_t attention_workspace(int32_t B, int32_t T, int32_t heads, int32_t kv_heads, int32_t dim);
 hipError_t launch_attention(const AttnArgs& a, int dtype, hipStream_t s);
 
