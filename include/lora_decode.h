@@ -61,8 +61,9 @@ int lora_q4_pack(const uint8_t *codes, int64_t ld_codes, const void *scales, int
                  const uint8_t *zeros, int64_t ld_zeros, int32_t n, int32_t k, int32_t group,
                  int dtype, void *packed, size_t packed_bytes, lora_q4_weight *w, void *stream);
 
-/* The product for T tokens.  Meant for decode and verification batches: a
- * weight beyond the caches is read from memory once for every 128 tokens.
+/* The product for T tokens.  Meant for decode and verification batches: tokens
+ * are taken in passes of 16 to 128, whichever form is cheapest for the shape, and
+ * every pass reads the weight.
  *   x  [T][ldx], ldx >= k;  y  [T][ldy], ldy >= n; both of the weight's dtype;
  *   x and y must not overlap
  *   workspace  lora_q4_matmul_workspace_bytes(T, n, k, group) bytes (0 for most

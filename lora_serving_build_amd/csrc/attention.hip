@@ -5,9 +5,9 @@
 // Rows: the nodes of a sequence times the G = heads / kv_heads query heads that
 // share a key head, so one pass over the keys serves all of them.  A line is one
 // row tile of one (sequence, key head), as long as the sequence's tiles of
-// positions.  The lines of a call, end to end, are cut into equal parts, one for
-// each workgroup that is resident at once: ragged lengths and few rows cost no
-// idle workgroups.  A line that lies in one part is finished there; the pieces
+// positions.  The lines of a call, end to end, are cut into equal parts, two for
+// each CU: ragged lengths and few rows cost no idle workgroups.  A line that lies
+// in one part is finished there; the pieces
 // of one that was cut are joined by a second kernel.
 #include "decode_kernels.h"
 #include "lora_device.h"
@@ -47,7 +47,10 @@ __device__ __forceinline__ int key_tiles(int len, int keys) { return max((len + 
 // Positions of a table up to which lines are not cut: four steps of eight waves.
 constexpr int kShortLine = 4 * 8 * kKeys;
 
-// Number of parts: the workgroups that are resident at once.
+// Number of parts: the workgroups that are resident at once with head dims of 65
+// to 128.  Dims up to 64 leave room for a third on a CU with up to 64 rows; of
+// dims above 128 the kernel for few rows has one on a CU, so its parts take two
+// rounds.
 constexpr int kParts = kCus * 2;
 
 // What a line costs besides its tiles, in tiles: its start (pages, first keys,
@@ -448,9 +451,11 @@ __device__ __forceinline__ void store_quad(const AttnArgs& a, int t, int h, int 
 // contexts so short that nothing needs to be cut and joined; else one of the
 // call's equal parts.
 // Bound by memory: 64 sequences of one token, 546 MB of keys and values in
-// 16-token pages, 64 heads over 8 key heads of 128: 114 us, 4.8 TB/s (a copy
-// reads and writes 4.8).  One token over 509 positions, 32 heads: 10.8 us of
-// dependent latencies (lengths, page, keys, softmax, join of the waves).
+// 16-token pages, 64 heads over 8 key heads of 128: 112 us, 4.9 TB/s (a copy
+// reads and writes 4.8).  One token over 509 positions, 32 heads: 10.4 us of
+// dependent latencies (lengths, page, keys, softmax, join of the waves).  Dim 256
+// takes all 256 vector registers and 170 to 230 accumulation registers: one wave
+// a SIMD.
 template <int DT, int DP, int W, bool WHOLE>
 __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(AttnArgs a) {
   constexpr int ROWS = 16, TILE = W * kKeys;
@@ -654,14 +659,16 @@ __global__ void __launch_bounds__(W* kWave, DP == 256 ? 1 : 2) attention_kernel(
 // ---------------------------------------------------------------- many rows
 // Waves of a workgroup take different rows (16 RT each) and share the tile of
 // positions in LDS, double-buffered; half of the next tile at a time is on its
-// way in registers while this one is used (all of it at once spills).  A tile
-// costs one barrier.
+// way in registers while this one is used (all of it at once spills 31 more).  A
+// tile costs one barrier.
 // 128 rows (48-node trees of 16 sequences, 6000 positions at most, 64 heads over
-// 8): 143 us for 67 GFLOP that rows see; bound by latencies: two waves a SIMD is
-// what 256 registers a wave leave, and without the loads 104 us remain, without
-// the exponentials 139, without either product 128 to 136.  18 us go to each 1000
-// positions of context, 40 to starts and ends of lines.  64 rows (two sequences
-// of 24 to 40 rows, 180000 positions, 369 MB): 76 us, 4.9 TB/s, bound by memory.
+// 8): 143 us for 67 GFLOP that rows see, 126 where keys and values are in the
+// last-level cache; two waves a SIMD is what 256 registers a wave leave (dim 128
+// spills 17 of them, 72 bytes a lane; dim 256 with 64 rows 41).  Without the loads
+// 104 us remained, without the exponentials 139, without either product 128 to
+// 136: bound by latencies.  18 us go to each 1000 positions of context, 40 to
+// starts and ends of lines.  64 rows (two sequences of 24 to 40 rows, 180000
+// positions, 369 MB): 77 us, 4.8 TB/s, bound by memory.
 template <int DT, int DP, int RT>
 __global__ void __launch_bounds__(kWaves* kWave, 2) attention_rows_kernel(AttnArgs a) {
   constexpr int ROWS = kWaves * 16 * RT;

@@ -204,8 +204,9 @@ __device__ __forceinline__ void q4_store(const Q4Args& a, int t, int c, f32x4 r)
 // workspace.  D of the
 // matrix core: lane l holds outputs 4 (l / 16) + 0..3 of token l % 16.
 // Bound by memory for wide weights (28672 x 8192, groups of 128 with zeros, 4
-// tokens: 29 us, 123 MB, 4.2 TB/s), by what the L2s deliver of x for more tokens,
-// by latencies for small ones (1024 x 4096, one token: 4.2 us).  More waves carry
+// tokens: 30 us, 123 MB, 4.1 TB/s; 25 us where the last call left the weight in
+// the last-level cache), by what the L2s deliver of x for more tokens, by
+// latencies for small ones (1024 x 4096, one token: 3.9 us).  More waves carry
 // it better than loads further ahead: two or three blocks in flight a wave cost
 // registers and measured up to half as slow again.
 constexpr int kWavesPerTile = 8;
@@ -318,9 +319,11 @@ __global__ void __launch_bounds__(kWavesPerTile* kWave) q4_kernel(Q4Args a) {
 // order.  The sums of x that a bfloat16 product needs are taken while x is
 // staged.
 // 8192 outputs of 28672 inputs, groups of 64, 16 tokens: 31 us for 126 MB (4.1
-// TB/s) and 5 us for the sums of 8 splits; waves that split k need 38.  128
-// tokens, 8192 x 8192: 38 us, 450 TFLOP/s, bound by the reads of x from LDS and
-// the scaling of the sub-groups' sums.
+// TB/s; 26 us from the last-level cache) and 5 us for the sums of 8 splits; waves
+// that split k need 38.  128 tokens, 8192 x 8192: 36 us, 480 TFLOP/s, bound by the
+// reads of x from LDS and the scaling of the sub-groups' sums.  Groups of 32 with
+// zeros spill: 28 registers in bfloat16 for 128 tokens, 11 for 16 (14 without
+// splits), and 5 in binary16 for 16.
 constexpr int kShareWaves = 8;
 
 // AGAIN: results that are not finite are taken again here (bfloat16 without
